@@ -47,6 +47,7 @@ EXPORTS = (
     "fa_splitkv_workspace_bytes", "fa_fwd_splitkv", "fa_fwd_splitkv_noalloc",
     "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_varlen", "fa_fp8_sizes", "fa_quantize_fp8", "fa_fwd_fp8",
     "fa_fp8_varlen_sizes", "fa_quantize_fp8_varlen", "fa_fwd_fp8_varlen", "fa_set_phase_buffer",
+    "fa_fwd_window", "fa_bwd_window_workspace_bytes", "fa_bwd_window",
 )
 
 
@@ -113,11 +114,15 @@ def load_library(path: str) -> ctypes.CDLL:
     L.fa_fwd_fp8_varlen.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, ci, cf,
                                     ci, vp]
     L.fa_set_phase_buffer.argtypes = [vp, ctypes.c_longlong]
+    L.fa_fwd_window.argtypes = [vp] * 5 + [ci] * 6 + [cf, ci, ci, vp, vp, ci, ci, vp]
+    L.fa_bwd_window_workspace_bytes.argtypes = [ci] * 8
+    L.fa_bwd_window.argtypes = [vp] * 9 + [ci] * 6 + [cf, ci, ci, vp, vp, ci, ci, vp, ctypes.c_longlong, vp]
     for name in EXPORTS:
         if name != "fa_strerror":
             getattr(L, name).restype = ci
     L.fa_splitkv_workspace_bytes.restype = ctypes.c_longlong
     L.fa_bwd_workspace_bytes.restype = ctypes.c_longlong
+    L.fa_bwd_window_workspace_bytes.restype = ctypes.c_longlong
     return L
 
 
@@ -218,6 +223,25 @@ def fa_fwd_fp8_varlen(q8, k8, vt8, q_scale, k_scale, v_scale, o, lse, cu_q, cu_k
                       max_k, H, Hk, d, scale, flags, stream) -> int:
     return lib().fa_fwd_fp8_varlen(q8, k8, vt8, q_scale, k_scale, v_scale, o, lse, cu_q, cu_k, B, total_q,
                                    total_k, max_q, max_k, H, Hk, d, scale, flags, stream)
+
+
+def fa_fwd_window(q, k, v, o, lse, B, Nq, Nk, H, Hk, d, scale, window, sinks, cu_q, cu_k, total_q, total_k,
+                  stream) -> int:
+    return lib().fa_fwd_window(q, k, v, o, lse, B, Nq, Nk, H, Hk, d, scale, window, sinks, cu_q, cu_k, total_q,
+                               total_k, stream)
+
+
+def bwd_window_workspace_bytes(B, Nq, Nk, H, Hk, d, window, sinks) -> int:
+    n = lib().fa_bwd_window_workspace_bytes(B, Nq, Nk, H, Hk, d, window, sinks)
+    if n < 0:
+        raise FaError(int(n), "fa_bwd_window_workspace_bytes")
+    return int(n)
+
+
+def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, B, Nq, Nk, H, Hk, d, scale, window, sinks, cu_q, cu_k, total_q,
+                  total_k, workspace, workspace_bytes, stream) -> int:
+    return lib().fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, B, Nq, Nk, H, Hk, d, scale, window, sinks, cu_q,
+                               cu_k, total_q, total_k, workspace, workspace_bytes, stream)
 
 
 def fa_check_status(stream=None):
@@ -628,3 +652,123 @@ def forward_fp8(t, scale=None, causal=False, out=None, lse=None, stream=None):
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_fp8")
     return out, lse
+
+
+def _same_device(first, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+
+
+def _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale):
+    """Checked shapes of the window entries: (B, Nq, Nk, H, Hk, d, scale, cu_q, cu_k, total_q, total_k)."""
+    import torch
+    packed = cu_seqlens_q is not None or cu_seqlens_k is not None
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_tensor(name, t, torch.bfloat16, 3 if packed else 4)
+    H, d = q.shape[-2:]
+    Hk = k.shape[-2]
+    if k.shape[-1] != d or v.shape != k.shape or (not packed and k.shape[0] != q.shape[0]):
+        raise ValueError("q/k/v shape mismatch")
+    if (Hk == 0 and H > 0) or (Hk > 0 and H % Hk):
+        raise ValueError("query heads (%d) must be a multiple of key/value heads (%d)" % (H, Hk))
+    _same_device(q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if not packed:
+        return q.shape[0], q.shape[1], k.shape[1], H, Hk, d, float(scale), None, None, 0, 0
+    if cu_seqlens_q is None or cu_seqlens_k is None or max_seqlen_q is None or max_seqlen_k is None:
+        raise ValueError("packed sequences need cu_seqlens_q/k and max_seqlen_q/k")
+    _check_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, 1)
+    _check_tensor("cu_seqlens_k", cu_seqlens_k, torch.int32, 1)
+    B = cu_seqlens_q.numel() - 1
+    if B < 0 or cu_seqlens_k.numel() != B + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k need B + 1 entries each")
+    return (B, int(max_seqlen_q), int(max_seqlen_k), H, Hk, d, float(scale), cu_seqlens_q.data_ptr(),
+            cu_seqlens_k.data_ptr(), q.shape[0], k.shape[0])
+
+
+def _int32(x):
+    """A count for the C entries; anything past their 32 bits means "all"."""
+    return min(int(x), 0x7fffffff)
+
+
+def _out_like(name, t, like):
+    """An output tensor of the caller's, checked, or a new one like `like`."""
+    import torch
+    if t is None:
+        return torch.empty_like(like)
+    _check_tensor(name, t, like.dtype, like.dim())
+    if t.shape != like.shape:
+        raise ValueError("%s shape mismatch" % name)
+    _same_device(like, **{name: t})
+    return t
+
+
+def _lse_out(lse, shape, like):
+    import torch
+    if lse is None:
+        return torch.empty(shape, dtype=torch.float32, device=like.device)
+    _check_tensor("lse", lse, torch.float32, 3)
+    if tuple(lse.shape) != tuple(shape):
+        raise ValueError("lse must be %s" % (tuple(shape),))
+    _same_device(like, lse=lse)
+    return lse
+
+
+def _workspace(t, need, device):
+    """The caller's workspace, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % (device,))
+    if t.numel() * t.element_size() < need:
+        raise ValueError("workspace holds %d bytes, %d are needed" % (t.numel() * t.element_size(), need))
+    return t
+
+
+def forward_window(q, k, v, window, sinks=0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None, max_seqlen_q=None,
+                   max_seqlen_k=None, out=None, lse=None, stream=None):
+    """Attention with a sliding window and sinks: the query at position p = i + Nk - Nq
+    sees the keys j <= p with p - j < window or j < sinks.
+
+    Tensors as forward_qk: dense q [B, Nq, H, d], k/v [B, Nk, Hk, d], or packed
+    [total, heads, d] with cu_seqlens_* and max_seqlen_*.  Returns (o, lse)."""
+    B, Nq, Nk, H, Hk, d, scale, cu_q, cu_k, total_q, total_k = _window_problem(
+        q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
+    out = _out_like("out", out, q)
+    lse = _lse_out(lse, (B, H, Nq), q)
+    with _on_device(q.device):
+        rc = fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq, Nk, H,
+                           Hk, d, scale, _int32(window), _int32(sinks), cu_q, cu_k, total_q, total_k,
+                           _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_window")
+    return out, lse
+
+
+def backward_window(q, k, v, o, lse, dout, window, sinks=0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None,
+                    max_seqlen_q=None, max_seqlen_k=None, workspace=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of forward_window given dout = dL/dO and its o and lse."""
+    import torch
+    B, Nq, Nk, H, Hk, d, scale, cu_q, cu_k, total_q, total_k = _window_problem(
+        q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
+    for name, t in (("o", o), ("dout", dout)):
+        _check_tensor(name, t, torch.bfloat16, q.dim())
+        if t.shape != q.shape:
+            raise ValueError("%s shape mismatch" % name)
+    _same_device(q, o=o, dout=dout)
+    lse = _lse_out(lse, (B, H, Nq), q)
+    window, sinks = _int32(window), _int32(sinks)
+    need = bwd_window_workspace_bytes(B, Nq, Nk, H, Hk, d, window, sinks)
+    workspace = _workspace(workspace, need, q.device)
+    dq, dk, dv = _out_like("dq", dq, q), _out_like("dk", dk, k), _out_like("dv", dv, v)
+    with _on_device(q.device):
+        rc = fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Nq, Nk, H, Hk, d, scale, window, sinks,
+                           cu_q, cu_k, total_q, total_k, workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_bwd_window")
+    return dq, dk, dv

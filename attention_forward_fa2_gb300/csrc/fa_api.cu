@@ -663,6 +663,26 @@ int check_split_problem(const void* q, const void* k, const void* v, void* o, fl
   Problem P{q, k, v, o, lse, B, Nq, Nk, H, Hk, d, scale, nullptr, nullptr, flags, nullptr};
   return validate(P);
 }
+
+// The per-device state, tensor-map encoder and error record for the entries in
+// other translation units (fa_launch.h).
+int host_device(HostDevice* out) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != FA_OK) return rc;
+  out->status = st->status;
+  out->num_sms = st->num_sms;
+  std::lock_guard<std::mutex> lk(g_mu);
+  out->timeout_ns = g_timeout_ns;
+  return FA_OK;
+}
+
+int host_encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                const cuuint32_t* box, CUtensorMapDataType dtype, CUtensorMapSwizzle swizzle) {
+  return encode(m, ptr, rank, dims, strides, box, dtype, swizzle);
+}
+
+int host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
 }  // namespace fa
 
 extern "C" {

@@ -119,6 +119,23 @@ int fp8_smem_bytes();
 int check_split_problem(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Nq,
                         int Nk, int H, int Hk, int d, float scale, int flags);
 
+// What the entries of other translation units need of the current device:
+// the status word, the SM count and the limit of device-side waits.  Returns
+// FA_OK or a negative FA_ERR_* code.
+struct HostDevice {
+  int* status;
+  int num_sms;
+  unsigned long long timeout_ns;
+};
+int host_device(HostDevice* out);
+// Tiled tensor map; dims / strides innermost first, strides in bytes for dims 1..rank-1.
+int host_encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                const cuuint32_t* box, CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+// Records a CUDA error for fa_last_cuda_error() and returns FA_ERR_CUDA.
+int host_cuda_fail(cudaError_t e);
+inline bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
 // Merge of the key splits (fa_combine.cuh); D in {64, 128}.
 cudaError_t launch_combine(int D, const float* ws_o, const float* ws_lse, int S, long long rows, int H,
                            int Nq, __nv_bfloat16* o, float* lse, cudaStream_t stream);

@@ -1,0 +1,272 @@
+// fa_window.cu -- C entries of attention with a sliding window and sinks
+// (fa_fwd_window, fa_bwd_window), kernel instantiations and launchers.
+#include "fa_window.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "fa.h"
+
+namespace fa {
+namespace {
+
+// Ring depth: two K/V slots of 64 KB fit beside the query tiles for d = 128,
+// three of 32 KB for d = 64 (as in the forward without a window).
+template <int D>
+constexpr int kWinStages = D == 128 ? 2 : 3;
+template <int D>
+constexpr int kWinBwdStages = D == 128 ? 2 : 4;
+
+template <int D, bool VARLEN, bool KPAD>
+cudaError_t launch_win(const WinLaunchArgs& a) {
+  auto* kern = &fa_win_kernel<D, kWinStages<D>, VARLEN, KPAD>;
+  constexpr int smem = SmemLayout<D, 128, kWinStages<D>>::kAlloc;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
+  if (e != cudaSuccess) return e;
+  const int grid = VARLEN ? a.p.num_units : std::min(a.p.num_units, a.num_sms);
+  kern<<<grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t dispatch_win(const WinLaunchArgs& a, bool varlen, bool kpad) {
+  if (kpad) return varlen ? launch_win<D, true, true>(a) : launch_win<D, false, true>(a);
+  return varlen ? launch_win<D, true, false>(a) : launch_win<D, false, false>(a);
+}
+
+// bf16 rows as a map: packed [rows, heads, d] (rank 3) or dense [B, n, heads, d]
+// (rank 4), boxes of `box_rows` rows of one head and 64 columns.
+int encode_rows(CUtensorMap* m, const void* ptr, bool packed, int B, int n, int heads, int d, int box_rows) {
+  const cuuint64_t row = static_cast<cuuint64_t>(heads) * d * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, row, row * n};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
+  return host_encode(m, ptr, packed ? 3 : 4, dims, strides, box);
+}
+
+template <int D, bool VARLEN>
+cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
+  cudaError_t e = cudaSuccess;
+  constexpr int kRows = 256 / (D / 8);
+  const long long prep = static_cast<long long>(p.B) * p.H * p.nq_pad;
+  const long long dq = static_cast<long long>(p.B) * p.H * p.Nq;
+  if (prep > 0) fa_win_prep_kernel<D, VARLEN><<<static_cast<unsigned>((prep + kRows - 1) / kRows), 256, 0, a.stream>>>(p);
+  auto* kern = &fa_win_bwd_kernel<D, kWinBwdStages<D>, VARLEN>;
+  constexpr int smem = BwdSmem<D, kWinBwdStages<D>>::kAlloc;
+  static std::atomic<unsigned long long> done{0};
+  e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
+  if (e != cudaSuccess) return e;
+  if (a.grid.x > 0) kern<<<a.grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_do, p);
+  const long long sink_rows = static_cast<long long>(p.B) * p.Hk * p.num_skb * kBwdBK;
+  if (sink_rows > 0) fa_win_sink_kernel<D, VARLEN><<<static_cast<unsigned>((sink_rows + 7) / 8), 256, 0, a.stream>>>(p);
+  if (dq > 0) fa_win_dq_kernel<D, VARLEN><<<static_cast<unsigned>((dq + kRows - 1) / kRows), 256, 0, a.stream>>>(p);
+  return cudaGetLastError();
+}
+
+// Checks shared by the forward and the backward entry.
+int check_sizes(int B, int Nq, int Nk, int H, int Hk, int d, float scale, int window, int sinks, const int* cu_q,
+                const int* cu_k, int total_q, int total_k) {
+  if (B < 0 || Nq < 0 || Nk < 0 || H < 0 || Hk < 0) return FA_ERR_INVALID_ARG;
+  if (H > 0 && (Hk == 0 || H % Hk != 0)) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if ((cu_q == nullptr) != (cu_k == nullptr)) return FA_ERR_INVALID_ARG;
+  if (cu_q && (total_q < 0 || total_k < 0)) return FA_ERR_INVALID_ARG;
+  if (misaligned(cu_q, 4) || misaligned(cu_k, 4)) return FA_ERR_ALIGN;
+  if (H > 65535 || B > 65535) return FA_ERR_INVALID_ARG;
+  const long long lim = 0x7fffffffLL;
+  if (static_cast<long long>(B) * Nq > lim || static_cast<long long>(B) * Nk > lim ||
+      static_cast<long long>(B) * H * Nq > lim)
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+struct BwdSizes {
+  int nq_pad, num_kb, num_skb, chunk_qb, num_chunks;
+  size_t dq_bytes, part_bytes;
+};
+
+// A chunk of a sink block walks about as many query blocks as the other units
+// (a window's worth and the two at its ends), at least 8 so that short windows
+// do not pay for many small chunks.
+BwdSizes bwd_sizes(int B, int Nq, int Nk, int H, int Hk, int d, int window, int sinks) {
+  BwdSizes z;
+  const int blocks = (Nq + kBwdBQ - 1) / kBwdBQ;
+  z.nq_pad = blocks * kBwdBQ;
+  z.num_kb = (Nk + kBwdBK - 1) / kBwdBK;
+  z.num_skb = (std::min(sinks, Nk) + kBwdBK - 1) / kBwdBK;
+  z.chunk_qb = std::max(8, std::min(window, std::max(Nk, 1)) / kBwdBQ + 2);
+  z.num_chunks = (blocks + z.chunk_qb - 1) / z.chunk_qb;
+  z.dq_bytes = static_cast<size_t>(B) * H * z.nq_pad * (static_cast<size_t>(d) + 2) * 4;
+  z.part_bytes = static_cast<size_t>(z.num_chunks) * B * Hk * z.num_skb * kBwdBK * 2 * d * 4;
+  return z;
+}
+
+}  // namespace
+
+int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v, int Hk, int d, bool kpad) {
+  WinParams& p = a.p;
+  const bool varlen = p.cu_q != nullptr;
+  const bool kpacked = varlen && !kpad;
+  const int nq = varlen ? p.total_q : p.Nq, nk = std::max(kpacked ? p.total_k : p.Nk, 1);
+  int e;
+  if ((e = encode_rows(&a.tm_q, q, varlen, p.B, nq, p.H, d, kBR)) != FA_OK) return e;
+  if ((e = encode_rows(&a.tm_o, p.o, varlen, p.B, nq, p.H, d, 32)) != FA_OK) return e;
+  if ((e = encode_rows(&a.tm_k, k, kpacked, p.B, nk, Hk, d, 128)) != FA_OK) return e;
+  if ((e = encode_rows(&a.tm_v, v, kpacked, p.B, nk, Hk, d, 128)) != FA_OK) return e;
+  p.group = p.H / Hk;
+  p.num_mblocks = (p.Nq + kBR * kQT - 1) / (kBR * kQT);
+  const long long units = static_cast<long long>(p.B) * p.H * p.num_mblocks;
+  if (units > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  p.num_units = static_cast<int>(units);
+  // A window longer than the keys changes nothing and is cut to them, so that
+  // the kernel's index arithmetic stays in 32 bits.
+  p.window = std::min(p.window, std::max(p.Nk, 1));
+  p.sinks = std::min(p.sinks, p.Nk);
+  p.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
+  p.rescale_threshold = 8.f;
+  const cudaError_t ce = d == 128 ? dispatch_win<128>(a, varlen, kpad) : dispatch_win<64>(a, varlen, kpad);
+  return ce == cudaSuccess ? FA_OK : host_cuda_fail(ce);
+}
+
+}  // namespace fa
+
+extern "C" {
+
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Nq, int Nk, int H, int Hk,
+                  int d, float scale, int window, int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                  int total_q, int total_k, void* stream) {
+  int rc = fa::check_sizes(B, Nq, Nk, H, Hk, d, scale, window, sinks, cu_seqlens_q, cu_seqlens_k, total_q, total_k);
+  if (rc != FA_OK) return rc;
+  const bool varlen = cu_seqlens_q != nullptr;
+  if (B == 0 || Nq == 0 || H == 0 || (varlen && total_q == 0)) return FA_OK;
+  if (!q || !o || !lse || ((!varlen || total_k > 0) && (!k || !v))) return FA_ERR_INVALID_ARG;
+  if (!varlen && Nk == 0) return FA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, k, v, static_cast<const void*>(o)})
+    if (fa::misaligned(ptr, 16)) return FA_ERR_ALIGN;
+  if (fa::misaligned(lse, 4)) return FA_ERR_ALIGN;
+  fa::HostDevice dev;
+  if ((rc = fa::host_device(&dev)) != FA_OK) return rc;
+  fa::WinLaunchArgs a;
+  std::memset(&a, 0, sizeof(a));
+  fa::WinParams& p = a.p;
+  p.B = B;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.H = H;
+  p.window = window;
+  p.sinks = sinks;
+  p.total_q = total_q;
+  p.total_k = total_k;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.lse = lse;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.scale = scale;
+  p.timeout_ns = dev.timeout_ns;
+  p.status = dev.status;
+  a.num_sms = dev.num_sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  // No keys at all (packed): the maps need an address, nothing is read from it.
+  const bool none = varlen && total_k == 0;
+  return fa::launch_window(a, q, none ? q : k, none ? q : v, Hk, d, false);
+}
+
+long long fa_bwd_window_workspace_bytes(int B, int Nq, int Nk, int H, int Hk, int d, int window, int sinks) {
+  const int rc = fa::check_sizes(B, Nq, Nk, H, Hk, d, 1.f, window, sinks, nullptr, nullptr, 0, 0);
+  if (rc != FA_OK) return rc;
+  const fa::BwdSizes z = fa::bwd_sizes(B, Nq, Nk, H, Hk, d, window, sinks);
+  return static_cast<long long>(z.dq_bytes + z.part_bytes);
+}
+
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                  void* dq, void* dk, void* dv, int B, int Nq, int Nk, int H, int Hk, int d, float scale, int window,
+                  int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k, int total_q, int total_k,
+                  void* workspace, long long workspace_bytes, void* stream) {
+  int rc = fa::check_sizes(B, Nq, Nk, H, Hk, d, scale, window, sinks, cu_seqlens_q, cu_seqlens_k, total_q, total_k);
+  if (rc != FA_OK) return rc;
+  const bool varlen = cu_seqlens_q != nullptr;
+  const int rows_q = varlen ? total_q : Nq, rows_k = varlen ? total_k : Nk;
+  if (B == 0 || H == 0 || (rows_q == 0 && rows_k == 0)) return FA_OK;
+  if (!varlen && Nk == 0) return FA_ERR_INVALID_ARG;  // queries without keys, as in the forward
+  if (rows_k > 0 && (!k || !v || !dk || !dv)) return FA_ERR_INVALID_ARG;
+  if (rows_q > 0 && (!q || !o || !dout || !lse || !dq)) return FA_ERR_INVALID_ARG;
+  const fa::BwdSizes z = fa::bwd_sizes(B, Nq, Nk, H, Hk, d, window, sinks);
+  if (static_cast<long long>(B) * H * z.nq_pad > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (z.dq_bytes + z.part_bytes > 0 &&
+      (!workspace || workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < z.dq_bytes + z.part_bytes))
+    return FA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, k, v, o, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                          static_cast<const void*>(dv), static_cast<const void*>(workspace)})
+    if (fa::misaligned(ptr, 16)) return FA_ERR_ALIGN;
+  if (fa::misaligned(lse, 4)) return FA_ERR_ALIGN;
+  fa::HostDevice dev;
+  if ((rc = fa::host_device(&dev)) != FA_OK) return rc;
+  fa::BwdLaunchArgs a;
+  std::memset(&a, 0, sizeof(a));
+  fa::WinBwdParams p;
+  std::memset(static_cast<void*>(&p), 0, sizeof(p));
+  p.B = B;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.H = H;
+  p.Hk = Hk;
+  p.group = H / Hk;
+  p.causal = 1;
+  p.nq_pad = z.nq_pad;
+  p.num_kb = z.num_kb;
+  p.num_skb = z.num_skb;
+  p.chunk_qb = z.chunk_qb;
+  p.num_chunks = z.num_chunks;
+  const long long sink_units = static_cast<long long>(B) * Hk * z.num_skb * z.num_chunks;
+  const long long units = sink_units + static_cast<long long>(B) * Hk * (z.num_kb - z.num_skb);
+  if (units > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  p.num_sink_units = static_cast<int>(sink_units);
+  p.num_units = static_cast<int>(units);
+  p.window = std::min(window, std::max(Nk, 1));
+  p.sinks = std::min(sinks, Nk);
+  p.total_q = total_q;
+  p.total_k = total_k;
+  p.o = static_cast<const __nv_bfloat16*>(o);
+  p.dout = static_cast<const __nv_bfloat16*>(dout);
+  p.lse = lse;
+  const size_t rows_pad = static_cast<size_t>(B) * H * z.nq_pad;
+  p.dq_acc = static_cast<float*>(workspace);
+  p.lse2 = p.dq_acc + rows_pad * d;
+  p.delta = p.lse2 + rows_pad;
+  p.part = p.delta + rows_pad;
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.scale = scale;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.timeout_ns = dev.timeout_ns;
+  p.status = dev.status;
+  // Maps need a valid address and extent even where nothing is read.
+  const void* qp = rows_q > 0 ? q : k;
+  const void* dop = rows_q > 0 ? dout : k;
+  const void* kp = rows_k > 0 ? k : q;
+  const void* vp = rows_k > 0 ? v : q;
+  const int hq = rows_q > 0 ? H : Hk, hk = rows_k > 0 ? Hk : H;
+  const int nq = rows_q > 0 ? rows_q : 1, nk = rows_k > 0 ? rows_k : 1;
+  if ((rc = fa::encode_rows(&a.tm_q, qp, varlen, B, nq, hq, d, fa::kBwdBQ)) != FA_OK) return rc;
+  if ((rc = fa::encode_rows(&a.tm_do, dop, varlen, B, nq, hq, d, fa::kBwdBQ)) != FA_OK) return rc;
+  if ((rc = fa::encode_rows(&a.tm_k, kp, varlen, B, nk, hk, d, fa::kBwdBK)) != FA_OK) return rc;
+  if ((rc = fa::encode_rows(&a.tm_v, vp, varlen, B, nk, hk, d, fa::kBwdBK)) != FA_OK) return rc;
+  a.grid = dim3(static_cast<unsigned>(std::min(p.num_units, dev.num_sms)));
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t ce;
+  if (d == 128)
+    ce = varlen ? fa::launch_win_bwd<128, true>(a, p) : fa::launch_win_bwd<128, false>(a, p);
+  else
+    ce = varlen ? fa::launch_win_bwd<64, true>(a, p) : fa::launch_win_bwd<64, false>(a, p);
+  return ce == cudaSuccess ? FA_OK : fa::host_cuda_fail(ce);
+}
+
+}  // extern "C"

@@ -1,0 +1,22 @@
+// fa_window.h -- launch interface of the sliding-window kernels (fa_window.cu),
+// used by their C entries and by the cache's forward for long query chunks.
+#pragma once
+#include "fa_launch.h"
+#include "fa_win_bwd_kernel.cuh"
+#include "fa_win_kernel.cuh"
+
+namespace fa {
+
+struct WinLaunchArgs {
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;
+  WinParams p;
+  int num_sms;
+  cudaStream_t stream;
+};
+
+// q, o: packed [total_q, H, d] (p.cu_q set) or dense [B, Nq, H, d]; k, v packed
+// [total_k, Hk, d], dense [B, Nk, Hk, d], or (kpad) dense with p.cu_k holding
+// a length per sequence and Nk a multiple of 128.  Encodes the maps and launches.
+int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v, int Hk, int d, bool kpad);
+
+}  // namespace fa

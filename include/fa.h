@@ -313,6 +313,46 @@ int fa_fwd_fp8_varlen(const void* q8, const void* k8, const void* vt8, const flo
                       float scale, int flags, void* stream);
 
 /*
+ * Attention with a sliding window and sinks: the causal mask ("GPU 内核与
+ * FlashAttention" §14.4, bottom-right aligned as in fa_fwd_ex) cut off behind a
+ * window, with the first keys of the sequence kept in sight.  Query i of a
+ * sequence stands at position p = i + len_k - len_q and sees the keys j <= p
+ * with p - j < window or j < sinks.  Key tiles that no row of a query tile
+ * sees are neither read nor multiplied, so the work grows with the window, not
+ * with the length.
+ *   window : keys in sight, the query's own among them; >= 1 (a window of Nk or
+ *            more is the causal mask).
+ *   sinks  : first keys of the sequence that stay visible; >= 0.
+ *   cu_seqlens_q / _k : NULL for dense tensors (layouts of fa_fwd_ex), or both
+ *            for packed sequences; total_q / total_k are then the packed rows of
+ *            q and k (ignored when dense).  A sequence whose rows do not fit the
+ *            totals or the maximum lengths Nq / Nk is reported as
+ *            FA_ERR_BAD_SEQLENS by fa_check_status() and its rows are neither
+ *            read nor written.
+ * fa_fwd_window -- o and lse as fa_fwd_ex; rows that see no key get o = 0 and
+ *            lse = -inf; rows past the last sequence are not written.
+ * fa_bwd_window -- dq, dk, dv as fa_bwd / fa_bwd_varlen, from the o and lse that
+ *            fa_fwd_window wrote with the same window and sinks.  dk and dv
+ *            come out the same on every run; dq adds the shares of the key
+ *            blocks in fp32 in no fixed order, as fa_bwd does.  workspace:
+ *            fa_bwd_window_workspace_bytes(...) bytes of device memory, 16-byte
+ *            aligned, fully rewritten by every call; calls that share one must
+ *            not overlap on the GPU.
+ * q, k, v and dout hold finite values: a masked key's weight is zero, and zero
+ * times an infinity or NaN in its tile is not.
+ * Errors as fa_fwd_ex and fa_bwd; window < 1, sinks < 0 or a negative total with
+ * cu_seqlens give FA_ERR_INVALID_ARG.
+ */
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Nq, int Nk, int H,
+                  int Hk, int d, float scale, int window, int sinks, const int* cu_seqlens_q,
+                  const int* cu_seqlens_k, int total_q, int total_k, void* stream);
+long long fa_bwd_window_workspace_bytes(int B, int Nq, int Nk, int H, int Hk, int d, int window, int sinks);
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                  void* dq, void* dk, void* dv, int B, int Nq, int Nk, int H, int Hk, int d, float scale, int window,
+                  int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k, int total_q, int total_k,
+                  void* workspace, long long workspace_bytes, void* stream);
+
+/*
  * fa_set_timeout_ns -- limit for every device-side wait (mbarrier waits) in
  * later launches.  On expiry the kernel records FA_ERR_TIMEOUT, drains its
  * own copies and MMAs, releases tensor memory and exits.  Default 1e9 ns.

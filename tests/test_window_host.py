@@ -1,0 +1,140 @@
+"""Host-side checks of the window entries: argument refusals, workspace sizes and
+the rule that names the query blocks of a key block and the key tiles of a query
+tile.  No call here launches GPU work."""
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import attention_forward_fa2_gb300 as fa
+from attention_forward_fa2_gb300 import build as fabuild
+
+A = 0x10000      # never-dereferenced addresses
+MIS = 0x10008
+
+
+@pytest.fixture(scope="module")
+def L():
+    fabuild.build()
+    return fa.lib()
+
+
+FWD = dict(q=A, k=A, v=A, o=A, lse=A, B=1, Nq=64, Nk=64, H=4, Hk=2, d=128, scale=0.1, window=16, sinks=2, cu_q=None,
+           cu_k=None, total_q=0, total_k=0, stream=None)
+BWD = dict(q=A, k=A, v=A, o=A, dout=A, lse=A, dq=A, dk=A, dv=A, B=1, Nq=64, Nk=64, H=4, Hk=2, d=128, scale=0.1,
+           window=16, sinks=2, cu_q=None, cu_k=None, total_q=0, total_k=0, ws=A, ws_bytes=1 << 30, stream=None)
+
+REFUSED = [
+    (dict(window=0), fa.FA_ERR_INVALID_ARG), (dict(window=-5), fa.FA_ERR_INVALID_ARG),
+    (dict(sinks=-1), fa.FA_ERR_INVALID_ARG), (dict(d=96), fa.FA_ERR_UNSUPPORTED),
+    (dict(scale=0.0), fa.FA_ERR_INVALID_ARG), (dict(scale=float("nan")), fa.FA_ERR_INVALID_ARG),
+    (dict(B=-1), fa.FA_ERR_INVALID_ARG), (dict(Hk=3), fa.FA_ERR_INVALID_ARG), (dict(Hk=0), fa.FA_ERR_INVALID_ARG),
+    (dict(cu_q=A), fa.FA_ERR_INVALID_ARG), (dict(cu_q=A, cu_k=A, total_q=-1), fa.FA_ERR_INVALID_ARG),
+    (dict(cu_q=A + 2, cu_k=A, total_q=9, total_k=9), fa.FA_ERR_ALIGN), (dict(q=0), fa.FA_ERR_INVALID_ARG),
+    (dict(v=MIS), fa.FA_ERR_ALIGN), (dict(lse=A + 2), fa.FA_ERR_ALIGN), (dict(Nk=0), fa.FA_ERR_INVALID_ARG),
+    (dict(H=70000, Hk=70000), fa.FA_ERR_INVALID_ARG), (dict(B=40000, Nq=65536), fa.FA_ERR_INVALID_ARG),
+]
+
+
+@pytest.mark.parametrize("kw,code", REFUSED)
+def test_refusals(L, kw, code):
+    assert fa.fa_fwd_window(*dict(FWD, **kw).values()) == code
+    assert fa.fa_bwd_window(*dict(BWD, **kw).values()) == code
+
+
+def test_backward_workspace(L):
+    def need(B, Nq, Nk, H, Hk, d, window, sinks):
+        pad = -(-Nq // 128) * 128
+        chunk = max(8, min(window, max(Nk, 1)) // 128 + 2)
+        chunks, skb = -(-pad // 128 // chunk) if pad else 0, -(-min(sinks, Nk) // 128)
+        chunks = -(-(pad // 128) // chunk)
+        return B * H * pad * (d + 2) * 4 + chunks * B * Hk * skb * 128 * 2 * d * 4
+    for case in ((2, 100, 300, 4, 2, 64, 50, 0), (1, 5000, 5000, 4, 1, 128, 256, 4), (1, 5000, 5000, 4, 1, 128, 256, 300),
+                 (3, 0, 40, 2, 2, 64, 9, 4), (1, 700, 700, 2, 2, 128, 10 ** 9, 10 ** 9)):
+        assert fa.bwd_window_workspace_bytes(*case) == need(*case), case
+    n = need(1, 64, 64, 4, 2, 128, 16, 2)
+    assert fa.fa_bwd_window(*dict(BWD, ws_bytes=n - 1).values()) == fa.FA_ERR_INVALID_ARG
+    assert fa.fa_bwd_window(*dict(BWD, ws=0, ws_bytes=n).values()) == fa.FA_ERR_INVALID_ARG
+    assert fa.fa_bwd_window(*dict(BWD, ws=MIS).values()) == fa.FA_ERR_ALIGN
+    with pytest.raises(fa.FaError):
+        fa.bwd_window_workspace_bytes(1, 64, 64, 4, 2, 128, 0, 2)
+
+
+def test_empty_calls_are_noops(L):
+    for kw in (dict(B=0), dict(H=0, Hk=0), dict(Nq=0)):
+        assert fa.fa_fwd_window(*dict(FWD, **kw).values()) == fa.FA_OK
+    for kw in (dict(B=0), dict(Nq=0, Nk=0), dict(cu_q=A, cu_k=A, total_q=0, total_k=0)):
+        assert fa.fa_bwd_window(*dict(BWD, **kw).values()) == fa.FA_OK
+
+
+def test_wrapper_refuses_cpu_tensors(L):
+    q = torch.zeros(1, 8, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.forward_window(q, q, q, 4)
+
+
+HARNESS = r"""
+#define __host__
+#define __device__
+#define __forceinline__ inline
+#include <algorithm>
+using std::min;
+static const int kBwdBK = 128, kBwdBQ = 128;
+%s
+%s
+extern "C" void query_blocks(int kb, int len_q, int len_k, int window, int sink, int* out) {
+  win_query_blocks(kb, len_q, len_k, window, sink != 0, out[0], out[1]);
+}
+extern "C" int sees(int kt, int lo, int hi, int nsk) { return win_sees(kt, lo, hi, nsk); }
+"""
+
+
+def _function(path, name):
+    src = open(os.path.join(fabuild.CSRC, path)).read()
+    at = src.index(name)
+    at = src.rindex("__host__", 0, at)
+    return src[at:src.index("\n}\n", at) + 3]
+
+
+def test_blocks_walked_are_those_that_hold_a_visible_pair(tmp_path):
+    """The index rules of the kernels, compiled for the host from their source, against the mask."""
+    import ctypes
+    code = HARNESS % (_function("fa_win_bwd_kernel.cuh", "win_query_blocks("), _function("fa_win_kernel.cuh", "win_sees("))
+    (tmp_path / "w.cpp").write_text(code)
+    so = str(tmp_path / "w.so")
+    subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-o", so, str(tmp_path / "w.cpp")], check=True)
+    lib = ctypes.CDLL(so)
+    out = (ctypes.c_int * 2)()
+    rng = np.random.default_rng(5)
+    for _ in range(300):
+        n_k = int(rng.integers(1, 1500))
+        n_q = int(rng.integers(1, 1500))
+        window = int(rng.integers(1, 700))
+        sinks = int(rng.choice([0, 1, 4, 130, 300]))
+        window, sinks = min(window, n_k), min(sinks, n_k)
+        p = np.arange(n_q)[:, None] + n_k - n_q
+        j = np.arange(n_k)[None]
+        mask = (j <= p) & ((p - j < window) | (j < sinks))
+        for kb in range(-(-n_k // 128)):
+            cols = mask[:, kb * 128:kb * 128 + 128]
+            rows = np.flatnonzero(cols.any(1))
+            sink = kb * 128 < sinks
+            lib.query_blocks(kb, n_q, n_k, window, int(sink), out)
+            got = set(range(out[0], out[0] + out[1]))
+            assert all(0 <= b < -(-n_q // 128) for b in got)
+            assert set((rows // 128).tolist()) <= got
+            if len(rows) and not sink:  # tight: no block without a visible pair but at the ends
+                assert len(got) <= len(set((rows // 128).tolist())) + 1
+        nsk = -(-sinks // 128)
+        for t in range(-(-n_q // 128)):
+            r = np.arange(t * 128, min(n_q, t * 128 + 128)) + n_k - n_q
+            if r[-1] < 0:
+                continue
+            lo, hi = max(0, int(r[0]) - window + 1) // 128, int(r[-1]) // 128
+            for kt in range(-(-n_k // 128)):
+                any_seen = mask[t * 128:t * 128 + 128, kt * 128:kt * 128 + 128].any()
+                assert bool(lib.sees(kt, lo, hi, nsk)) >= bool(any_seen)
+                if not any_seen:
+                    assert not lib.sees(kt, lo, hi, nsk)
