@@ -36,6 +36,7 @@ FA_ERR_TIMEOUT = -5
 FA_ERR_NO_DEVICE = -6
 FA_ERR_BAD_SEQLENS = -7
 FA_ERR_SCRATCH_LIMIT = -8
+FA_ERR_BAD_PAGE = -9
 
 FA_FLAG_CAUSAL = 1
 
@@ -48,6 +49,7 @@ EXPORTS = (
     "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_varlen", "fa_fp8_sizes", "fa_quantize_fp8", "fa_fwd_fp8",
     "fa_fp8_varlen_sizes", "fa_quantize_fp8_varlen", "fa_fwd_fp8_varlen", "fa_set_phase_buffer",
     "fa_fwd_window", "fa_bwd_window_workspace_bytes", "fa_bwd_window",
+    "fa_kvcache_append", "fa_kvcache_workspace_bytes", "fa_fwd_kvcache",
 )
 
 
@@ -117,12 +119,18 @@ def load_library(path: str) -> ctypes.CDLL:
     L.fa_fwd_window.argtypes = [vp] * 5 + [ci] * 6 + [cf, ci, ci, vp, vp, ci, ci, vp]
     L.fa_bwd_window_workspace_bytes.argtypes = [ci] * 8
     L.fa_bwd_window.argtypes = [vp] * 9 + [ci] * 6 + [cf, ci, ci, vp, vp, ci, ci, vp, ctypes.c_longlong, vp]
+    ll = ctypes.c_longlong
+    L.fa_kvcache_append.argtypes = [vp, vp, ll, ll, vp, ll, vp, vp, vp, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, ci, ci,
+                                    ci, ci, ci, ci, ci, ci, ci, vp]
+    L.fa_kvcache_workspace_bytes.argtypes = [ci] * 9
+    L.fa_fwd_kvcache.argtypes = [vp] * 10 + [ci] * 10 + [cf, ci, ci, ci, vp, ll, vp]
     for name in EXPORTS:
         if name != "fa_strerror":
             getattr(L, name).restype = ci
     L.fa_splitkv_workspace_bytes.restype = ctypes.c_longlong
     L.fa_bwd_workspace_bytes.restype = ctypes.c_longlong
     L.fa_bwd_window_workspace_bytes.restype = ctypes.c_longlong
+    L.fa_kvcache_workspace_bytes.restype = ctypes.c_longlong
     return L
 
 
@@ -242,6 +250,21 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, B, Nq, Nk, H, Hk, d, scale,
                   total_k, workspace, workspace_bytes, stream) -> int:
     return lib().fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, B, Nq, Nk, H, Hk, d, scale, window, sinks, cu_q,
                                cu_k, total_q, total_k, workspace, workspace_bytes, stream)
+
+
+def fa_kvcache_append(*args) -> int:
+    return lib().fa_kvcache_append(*args)
+
+
+def kvcache_workspace_bytes(B, max_seqlen_q, max_seqlen_k, H, Hk, d, causal=True, window=0, sinks=0) -> int:
+    n = lib().fa_kvcache_workspace_bytes(B, max_seqlen_q, max_seqlen_k, H, Hk, d, int(bool(causal)), window, sinks)
+    if n < 0:
+        raise FaError(int(n), "fa_kvcache_workspace_bytes")
+    return int(n)
+
+
+def fa_fwd_kvcache(*args) -> int:
+    return lib().fa_fwd_kvcache(*args)
 
 
 def fa_check_status(stream=None):
@@ -772,3 +795,183 @@ def backward_window(q, k, v, o, lse, dout, window, sinks=0, scale=None, cu_seqle
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_window")
     return dq, dk, dv
+
+
+class KvCache:
+    """A paged e4m3 key/value cache: codes k8, v8 (uint8 [num_pages, Hk, page, d],
+    page 16, 32, 64 or 128) and scales k_scale, v_scale (fp32 [num_pages, Hk]).
+    Code c of a page and head stands for c * scale."""
+
+    def __init__(self, k8, v8, k_scale, v_scale):
+        import torch
+        for name, t in (("k8", k8), ("v8", v8)):
+            _check_tensor(name, t, torch.uint8, 4)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _check_tensor(name, t, torch.float32, 2)
+        self.num_pages, self.Hk, self.page, self.d = k8.shape
+        if v8.shape != k8.shape or k_scale.shape != k8.shape[:2] or v_scale.shape != k8.shape[:2]:
+            raise ValueError("codes are [num_pages, Hk, page, d], scales [num_pages, Hk]")
+        _same_device(k8, v8=v8, k_scale=k_scale, v_scale=v_scale)
+        self.k8, self.v8, self.k_scale, self.v_scale = k8, v8, k_scale, v_scale
+
+    @classmethod
+    def empty(cls, num_pages, page, Hk, d, device="cuda"):
+        """A cache of unwritten pages (append_kvcache sets a page's scale with its first token)."""
+        import torch
+        codes = [torch.zeros((num_pages, Hk, page, d), dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros((num_pages, Hk), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+def _token_rows(name, t, ndim):
+    """Distance in elements between the token rows of t [B, n, heads, d] or [total, heads, d]."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
+    heads, d = t.shape[-2:]
+    s = t.stride()
+    if (d > 1 and s[-1] != 1) or (heads > 1 and s[-2] != d):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    if ndim == 3:
+        return s[0] if t.shape[0] > 1 else heads * d
+    B, n = t.shape[:2]
+    if B > 1 and n > 1 and s[0] != n * s[1]:
+        raise ValueError("%s: tokens must be evenly spaced" % name)
+    return s[1] if n > 1 else s[0] if B > 1 else heads * d
+
+
+def _lengths(name, t, B, like):
+    import torch
+    _check_tensor(name, t, torch.int32, 1)
+    if t.numel() != B:
+        raise ValueError("%s needs %d entries" % (name, B))
+    _same_device(like, **{name: t})
+
+
+def _block_table(t, B, like):
+    import torch
+    _check_tensor("block_table", t, torch.int32, 2)
+    if t.shape[0] != B:
+        raise ValueError("block_table needs %d rows" % B)
+    _same_device(like, block_table=t)
+    return t.shape[1]
+
+
+def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=None, interleaved=False, cu_seqlens=None,
+                   max_seqlen=None, q_out=None, stream=None):
+    """Write new keys and values behind the cached tokens of every sequence, rotating
+    keys (and q) to their positions on the way.
+
+    k, v: [B, n, Hk, d], or packed [total, Hk, d] with cu_seqlens (int32 [B + 1]) and
+    max_seqlen; bf16, token rows may be strided.  cache_lens: int32 [B], tokens held
+    before the call (not changed).  cos, sin: fp32 [positions, rot / 2], or None for
+    no rotation; pairs are halves, or neighbours when interleaved.  q: [.., H, d] with
+    k's tokens.  Returns the rotated q (q_out or a new contiguous tensor), None
+    without q."""
+    import torch
+    packed = cu_seqlens is not None
+    ndim = 3 if packed else 4
+    k_stride, v_stride = _token_rows("k", k, ndim), _token_rows("v", v, ndim)
+    Hk, d = k.shape[-2:]
+    if v.shape != k.shape or Hk != cache.Hk or d != cache.d:
+        raise ValueError("k, v and the cache differ in shape")
+    _same_device(cache.k8, k=k, v=v, q=q, cos=cos, sin=sin, q_out=q_out, cu_seqlens=cu_seqlens)
+    if packed:
+        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, 1)
+        if max_seqlen is None:
+            raise ValueError("max_seqlen is required with cu_seqlens")
+        B, total, n = cu_seqlens.numel() - 1, k.shape[0], int(max_seqlen)
+    else:
+        B, n = k.shape[:2]
+        total = B * n
+    _lengths("cache_lens", cache_lens, B, k)
+    width = _block_table(block_table, B, k)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    rot = max_pos = 0
+    if cos is not None:
+        _check_tensor("cos", cos, torch.float32, 2)
+        _check_tensor("sin", sin, torch.float32, 2)
+        if sin.shape != cos.shape:
+            raise ValueError("cos and sin differ in shape")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    H = q_stride = 0
+    if q is not None:
+        q_stride = _token_rows("q", q, ndim)
+        if q.shape[:-2] != k.shape[:-2] or q.shape[-1] != d:
+            raise ValueError("q and k differ in their tokens")
+        H = q.shape[-2]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _check_tensor("q_out", q_out, torch.bfloat16, ndim)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out shape mismatch")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _on_device(k.device):
+        rc = fa_kvcache_append(
+            k.data_ptr(), v.data_ptr(), k_stride, v_stride, q.data_ptr() if q is not None else None, q_stride,
+            q_out.data_ptr() if q is not None else None, cos.data_ptr() if rot else None,
+            sin.data_ptr() if rot else None, max_pos, rot, int(bool(interleaved)), cache.k8.data_ptr(),
+            cache.v8.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), block_table.data_ptr(),
+            cache_lens.data_ptr(), cu_seqlens.data_ptr() if packed else None, B, total, n, H, Hk, d, cache.page,
+            cache.num_pages, width, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_kvcache_append")
+    return q_out
+
+
+def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, causal=True, window=0, sinks=0,
+                    cu_seqlens_q=None, max_seqlen_q=None, workspace=None, out=None, lse=None, stream=None):
+    """Attention over a paged e4m3 cache.
+
+    q: [B, n, H, d], or packed [total_q, H, d] with cu_seqlens_q and max_seqlen_q.
+    seq_lens: int32 [B], tokens of each sequence (the queries' own included), at most
+    max_seqlen_k.  causal: query i of n stands at position seq_lens - n + i; window
+    (0: none) and sinks as forward_window.  Returns (o like q, lse fp32 [B, H, n])."""
+    import torch
+    packed = cu_seqlens_q is not None
+    _check_tensor("q", q, torch.bfloat16, 3 if packed else 4)
+    H, d = q.shape[-2:]
+    Hk = cache.Hk
+    if d != cache.d:
+        raise ValueError("q and the cache differ in head dimension")
+    if (Hk == 0 and H > 0) or (Hk > 0 and H % Hk):
+        raise ValueError("query heads (%d) must be a multiple of key/value heads (%d)" % (H, Hk))
+    if packed:
+        _check_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, 1)
+        if max_seqlen_q is None:
+            raise ValueError("max_seqlen_q is required with cu_seqlens_q")
+        B, n, total = cu_seqlens_q.numel() - 1, int(max_seqlen_q), q.shape[0]
+    else:
+        B, n = q.shape[:2]
+        total = B * n
+    _same_device(cache.k8, q=q, cu_seqlens_q=cu_seqlens_q)
+    _lengths("seq_lens", seq_lens, B, q)
+    width = _block_table(block_table, B, q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    causal, window, sinks, max_k = int(bool(causal)), _int32(window), _int32(sinks), int(max_seqlen_k)
+    out = _out_like("out", out, q)
+    lse = _lse_out(lse, (B, H, n), q)
+    with _on_device(q.device):
+        need = kvcache_workspace_bytes(B, n, max_k, H, Hk, d, causal, window, sinks)
+        if workspace is not None or need > 0:
+            workspace = _workspace(workspace, need, q.device)
+        rc = fa_fwd_kvcache(
+            q.data_ptr(), cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(),
+            cache.v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            cu_seqlens_q.data_ptr() if packed else None, out.data_ptr(), lse.data_ptr(), B, total, n, max_k, H, Hk, d,
+            cache.page, cache.num_pages, width, float(scale), causal, window, sinks,
+            workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_kvcache")
+    return out, lse

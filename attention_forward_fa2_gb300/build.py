@@ -25,9 +25,9 @@ LIB_PHASE = os.path.join(PKG, "libfa_gb300_phase.so")
 UNITS = ("fa_api.cu", "fa_fwd_d128.cu", "fa_fwd_d128_bc64.cu", "fa_fwd_d128_causal.cu",
          "fa_fwd_d64.cu", "fa_fwd_d64_bc64.cu", "fa_fwd_d64_causal.cu", "fa_fwd_quad.cu",
          "fa_fwd_split.cu", "fa_static_scratch.cu", "fa_bwd.cu", "fa_fp8.cu",
-         "fa_fp8_varlen.cu", "fa_window.cu")
+         "fa_fp8_varlen.cu", "fa_window.cu", "fa_kv_append.cu", "fa_kv_attn.cu")
 HEADERS = ("ptx.cuh", "fa_fwd_kernel.cuh", "fa_launch.h", "fa_combine.cuh", "fa_bwd_kernel.cuh",
-           "fa_win_kernel.cuh", "fa_win_bwd_kernel.cuh", "fa_window.h")
+           "fa_win_kernel.cuh", "fa_win_bwd_kernel.cuh", "fa_window.h", "fa_kvcache.h", "fa_kv_attn.cuh")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -48,6 +48,7 @@ extern "C" {
 #define FA_ERR_NO_DEVICE (-6)    /* no CUDA device is visible                           */
 #define FA_ERR_BAD_SEQLENS (-7)  /* cu_seqlens inconsistent with the maximum lengths    */
 #define FA_ERR_SCRATCH_LIMIT (-8) /* problem needs more than the fixed 16 MiB scratch   */
+#define FA_ERR_BAD_PAGE (-9)     /* block_table names a page outside the cache          */
 
 /*
  * fa_fwd -- attention forward, self-attention shapes (Nq = Nk = N).
@@ -351,6 +352,74 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
                   void* dq, void* dk, void* dv, int B, int Nq, int Nk, int H, int Hk, int d, float scale, int window,
                   int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k, int total_q, int total_k,
                   void* workspace, long long workspace_bytes, void* stream);
+
+/*
+ * Paged e4m3 key/value cache, for serving: fa_kvcache_append writes it,
+ * fa_fwd_kvcache attends over it.  (§15.5's block quantisation, with blocks that
+ * are pages; the pages have no counterpart for the cache itself.)
+ *   k8, v8           : uint8 [num_pages, Hk, page, d] e4m3 codes; page 16, 32, 64 or 128.
+ *   k_scale, v_scale : fp32 [num_pages, Hk]; a code c of the page stands for
+ *                      c * scale.  The append writes powers of two from 2^-64 to
+ *                      2^120.
+ *   block_table      : int32 [B, table_width]; token t of sequence b lies in page
+ *                      block_table[b][t / page], slot t % page.  Only entries up to
+ *                      a sequence's last token are read.
+ *   Device-side checks: a length or cu_seqlens entry that does not fit the input,
+ *   the table or the maximum lengths is reported as FA_ERR_BAD_SEQLENS by
+ *   fa_check_status() and the sequence is left out; a page outside the cache that
+ *   would be read or written is reported as FA_ERR_BAD_PAGE and not touched (the
+ *   outputs of its sequence are then undefined).
+ *
+ * fa_kvcache_append -- new tokens of every sequence into the cache.
+ *   k, v    : bf16, token rows of Hk heads of d elements, rows k_stride / v_stride
+ *             elements apart (a fused projection's output is read in place);
+ *             strides multiples of 8, rows not overlapping.
+ *   q       : bf16 token rows of H heads (q_stride apart), rotated into q_out
+ *             [total, H, d] like the keys; or both NULL.  q_out may be q itself
+ *             when q_stride is H * d.
+ *   cos, sin: fp32 [max_pos, rot / 2]; element pair c of a key or query at position
+ *             p is turned by (cos[p][c], sin[p][c]).  rot: a multiple of 16, at most
+ *             d, 0 for no rotation (cos, sin unused); elements past rot pass through.
+ *             interleaved 0: pair c is elements (c, c + rot / 2); 1: (2c, 2c + 1).
+ *   cache_lens : int32 [B], tokens of each sequence before the call (not changed);
+ *             the new tokens take the positions and slots behind them.
+ *   cu_seqlens : int32 [B + 1] offsets of each sequence's new tokens in the input
+ *             rows, or NULL for max_new tokens each (total = B * max_new).
+ *   The scale of a page and head is the smallest power of two that holds its new
+ *   values (infinities saturate and NaN is kept; neither counts), or its present
+ *   scale where that is larger and the page already held tokens.  When it grows,
+ *   the older codes are rounded to it (exact but for subnormal codes).
+ *   A page must belong to one sequence of the call: two that write to the same
+ *   page race.  Nothing is allocated; the call can be captured into a graph.
+ *
+ * fa_fwd_kvcache -- attention of the queries [total_q, H, d] (cu_seqlens_q), or
+ *   [B, max_seqlen_q, H, d] (NULL), over seq_lens[b] cached tokens (those of the
+ *   queries included).  causal 1: query i of n stands at position seq_lens[b] - n
+ *   + i and sees the keys up to it; 0: all keys.  window > 0 (causal only): only
+ *   keys less than `window` behind it, and the first `sinks`; pages that no
+ *   query sees are not read and need not hold valid entries.
+ *   o, lse  : as fa_fwd_ex (lse fp32 [B, H, max_seqlen_q], entries past a
+ *             sequence's queries not written); rows without keys get 0 and -inf.
+ *   q is used in full bf16 precision; weights are rounded to f16 (short queries)
+ *   or bf16.  Slots behind the last token may hold anything.
+ *   workspace : fa_kvcache_workspace_bytes(...) bytes of device memory, 16-byte
+ *             aligned, rewritten by every call (NULL when 0); calls that share one
+ *             must not overlap on the GPU.  Its size depends on the current device.
+ *             Long query chunks (more than 64 query rows per key/value head)
+ *             keep a bf16 copy of the visible keys there.
+ */
+int fa_kvcache_append(const void* k, const void* v, long long k_stride, long long v_stride, const void* q,
+                      long long q_stride, void* q_out, const float* cos, const float* sin, int max_pos, int rot,
+                      int interleaved, void* k8, void* v8, float* k_scale, float* v_scale, const int* block_table,
+                      const int* cache_lens, const int* cu_seqlens, int B, int total, int max_new, int H, int Hk, int d,
+                      int page, int num_pages, int table_width, void* stream);
+long long fa_kvcache_workspace_bytes(int B, int max_seqlen_q, int max_seqlen_k, int H, int Hk, int d, int causal,
+                                     int window, int sinks);
+int fa_fwd_kvcache(const void* q, const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                   const int* block_table, const int* seq_lens, const int* cu_seqlens_q, void* o, float* lse, int B,
+                   int total_q, int max_seqlen_q, int max_seqlen_k, int H, int Hk, int d, int page, int num_pages,
+                   int table_width, float scale, int causal, int window, int sinks, void* workspace,
+                   long long workspace_bytes, void* stream);
 
 /*
  * fa_set_timeout_ns -- limit for every device-side wait (mbarrier waits) in
