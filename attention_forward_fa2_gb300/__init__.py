@@ -257,7 +257,8 @@ def fa_kvcache_append(*args) -> int:
 
 
 def kvcache_workspace_bytes(B, max_seqlen_q, max_seqlen_k, H, Hk, d, causal=True, window=0, sinks=0) -> int:
-    n = lib().fa_kvcache_workspace_bytes(B, max_seqlen_q, max_seqlen_k, H, Hk, d, int(bool(causal)), window, sinks)
+    n = (_lib or lib()).fa_kvcache_workspace_bytes(B, max_seqlen_q, max_seqlen_k, H, Hk, d, 1 if causal else 0, window,
+                                                   sinks)
     if n < 0:
         raise FaError(int(n), "fa_kvcache_workspace_bytes")
     return int(n)
@@ -677,38 +678,79 @@ def forward_fp8(t, scale=None, causal=False, out=None, lse=None, stream=None):
     return out, lse
 
 
-def _same_device(first, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+# The cache and window entries serve single tokens, where a call's host time is what
+# counts: their checks read each attribute once, and the slow, telling form of a check
+# runs only to raise.
+def _dense(name, t, dtype, ndim, device):
+    """t is a contiguous tensor of this type, rank and device (else raises); its address."""
+    try:
+        if t.dtype is dtype and t.device == device and t.dim() == ndim and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check_tensor(name, t, dtype, ndim)
+    raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+
+
+def _cuda_device(name, t):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
+    return t.device
+
+
+def _stream_scope(stream, t):
+    """Makes `stream` current: what the call allocates then belongs to it, and is not handed to
+    another stream's work while this one's kernels run."""
+    import torch
+    if _cuda_device("the first tensor", t) != stream.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return torch.cuda.stream(stream)
+
+
+def _launch(entry, device, args):
+    """Call a C entry (its last argument is the stream) on the current stream of `device`."""
+    from torch import _C
+    index = device.index
+    fn = getattr(_lib or lib(), entry)
+    if index == _C._cuda_getDevice():
+        rc = fn(*args, _C._cuda_getCurrentRawStream(index))
+    else:
+        import torch
+        with torch.cuda.device(device):
+            rc = fn(*args, _C._cuda_getCurrentRawStream(index))
+    if rc != FA_OK:
+        raise FaError(rc, entry)
 
 
 def _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale):
-    """Checked shapes of the window entries: (B, Nq, Nk, H, Hk, d, scale, cu_q, cu_k, total_q, total_k)."""
+    """Checked arguments of the window entries: (device, addresses of q, k, v, (B, Nq, Nk, H, Hk,
+    d, scale), (cu_q, cu_k, total_q, total_k))."""
     import torch
     packed = cu_seqlens_q is not None or cu_seqlens_k is not None
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_tensor(name, t, torch.bfloat16, 3 if packed else 4)
-    H, d = q.shape[-2:]
-    Hk = k.shape[-2]
-    if k.shape[-1] != d or v.shape != k.shape or (not packed and k.shape[0] != q.shape[0]):
+    device = _cuda_device("q", q)
+    ndim = 3 if packed else 4
+    ptrs = tuple(_dense(name, t, torch.bfloat16, ndim, device) for name, t in (("q", q), ("k", k), ("v", v)))
+    qs, ks = q.shape, k.shape
+    H, d = qs[-2:]
+    Hk = ks[-2]
+    if ks[-1] != d or v.shape != ks or (not packed and ks[0] != qs[0]):
         raise ValueError("q/k/v shape mismatch")
     if (Hk == 0 and H > 0) or (Hk > 0 and H % Hk):
         raise ValueError("query heads (%d) must be a multiple of key/value heads (%d)" % (H, Hk))
-    _same_device(q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if not packed:
-        return q.shape[0], q.shape[1], k.shape[1], H, Hk, d, float(scale), None, None, 0, 0
+        return device, ptrs, (qs[0], qs[1], ks[1], H, Hk, d, scale), (None, None, 0, 0)
     if cu_seqlens_q is None or cu_seqlens_k is None or max_seqlen_q is None or max_seqlen_k is None:
         raise ValueError("packed sequences need cu_seqlens_q/k and max_seqlen_q/k")
-    _check_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, 1)
-    _check_tensor("cu_seqlens_k", cu_seqlens_k, torch.int32, 1)
+    cu = (_dense("cu_seqlens_q", cu_seqlens_q, torch.int32, 1, device),
+          _dense("cu_seqlens_k", cu_seqlens_k, torch.int32, 1, device))
     B = cu_seqlens_q.numel() - 1
     if B < 0 or cu_seqlens_k.numel() != B + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k need B + 1 entries each")
-    return (B, int(max_seqlen_q), int(max_seqlen_k), H, Hk, d, float(scale), cu_seqlens_q.data_ptr(),
-            cu_seqlens_k.data_ptr(), q.shape[0], k.shape[0])
+    return device, ptrs, (B, int(max_seqlen_q), int(max_seqlen_k), H, Hk, d, scale), cu + (qs[0], ks[0])
 
 
 def _int32(x):
@@ -716,39 +758,41 @@ def _int32(x):
     return min(int(x), 0x7fffffff)
 
 
-def _out_like(name, t, like):
+def _out_like(name, t, like, device):
     """An output tensor of the caller's, checked, or a new one like `like`."""
     import torch
     if t is None:
         return torch.empty_like(like)
-    _check_tensor(name, t, like.dtype, like.dim())
+    _dense(name, t, like.dtype, like.dim(), device)
     if t.shape != like.shape:
         raise ValueError("%s shape mismatch" % name)
-    _same_device(like, **{name: t})
     return t
 
 
-def _lse_out(lse, shape, like):
+def _lse_out(lse, shape, device):
     import torch
     if lse is None:
-        return torch.empty(shape, dtype=torch.float32, device=like.device)
-    _check_tensor("lse", lse, torch.float32, 3)
-    if tuple(lse.shape) != tuple(shape):
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    _dense("lse", lse, torch.float32, 3, device)
+    if lse.shape != shape:
         raise ValueError("lse must be %s" % (tuple(shape),))
-    _same_device(like, lse=lse)
     return lse
 
 
 def _workspace(t, need, device):
-    """The caller's workspace, checked, or a new one."""
+    """The caller's workspace, checked, or a new one: (address, bytes, tensor)."""
     import torch
     if t is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if need == 0:
+            return None, 0, None
+        t = torch.empty(need, dtype=torch.uint8, device=device)
+        return t.data_ptr(), need, t
     if t.device != device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % (device,))
-    if t.numel() * t.element_size() < need:
-        raise ValueError("workspace holds %d bytes, %d are needed" % (t.numel() * t.element_size(), need))
-    return t
+    n = t.numel() * t.element_size()
+    if n < need:
+        raise ValueError("workspace holds %d bytes, %d are needed" % (n, need))
+    return t.data_ptr(), n, t
 
 
 def forward_window(q, k, v, window, sinks=0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None, max_seqlen_q=None,
@@ -758,16 +802,15 @@ def forward_window(q, k, v, window, sinks=0, scale=None, cu_seqlens_q=None, cu_s
 
     Tensors as forward_qk: dense q [B, Nq, H, d], k/v [B, Nk, Hk, d], or packed
     [total, heads, d] with cu_seqlens_* and max_seqlen_*.  Returns (o, lse)."""
-    B, Nq, Nk, H, Hk, d, scale, cu_q, cu_k, total_q, total_k = _window_problem(
-        q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
-    out = _out_like("out", out, q)
-    lse = _lse_out(lse, (B, H, Nq), q)
-    with _on_device(q.device):
-        rc = fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq, Nk, H,
-                           Hk, d, scale, _int32(window), _int32(sinks), cu_q, cu_k, total_q, total_k,
-                           _stream_handle(stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_fwd_window")
+    if stream is not None:
+        with _stream_scope(stream, q):
+            return forward_window(q, k, v, window, sinks, scale, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                  out, lse)
+    device, ptrs, sizes, cu = _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
+    out = _out_like("out", out, q, device)
+    lse = _lse_out(lse, (sizes[0], sizes[3], sizes[1]), device)
+    _launch("fa_fwd_window", device,
+            (*ptrs, out.data_ptr(), lse.data_ptr(), *sizes, _int32(window), _int32(sinks), *cu))
     return out, lse
 
 
@@ -775,25 +818,24 @@ def backward_window(q, k, v, o, lse, dout, window, sinks=0, scale=None, cu_seqle
                     max_seqlen_q=None, max_seqlen_k=None, workspace=None, dq=None, dk=None, dv=None, stream=None):
     """Gradients (dq, dk, dv) of forward_window given dout = dL/dO and its o and lse."""
     import torch
-    B, Nq, Nk, H, Hk, d, scale, cu_q, cu_k, total_q, total_k = _window_problem(
-        q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
-    for name, t in (("o", o), ("dout", dout)):
-        _check_tensor(name, t, torch.bfloat16, q.dim())
-        if t.shape != q.shape:
-            raise ValueError("%s shape mismatch" % name)
-    _same_device(q, o=o, dout=dout)
-    lse = _lse_out(lse, (B, H, Nq), q)
+    if stream is not None:
+        with _stream_scope(stream, q):
+            return backward_window(q, k, v, o, lse, dout, window, sinks, scale, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                   max_seqlen_k, workspace, dq, dk, dv)
+    device, ptrs, sizes, cu = _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
+    more = tuple(_dense(name, t, torch.bfloat16, q.dim(), device) for name, t in (("o", o), ("dout", dout)))
+    if o.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("o and dout must have q's shape")
+    B, Nq, Nk, H, Hk, d = sizes[:6]
+    if lse is None:
+        raise TypeError("lse must be a torch.Tensor")
+    _lse_out(lse, (B, H, Nq), device)
     window, sinks = _int32(window), _int32(sinks)
-    need = bwd_window_workspace_bytes(B, Nq, Nk, H, Hk, d, window, sinks)
-    workspace = _workspace(workspace, need, q.device)
-    dq, dk, dv = _out_like("dq", dq, q), _out_like("dk", dk, k), _out_like("dv", dv, v)
-    with _on_device(q.device):
-        rc = fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
-                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Nq, Nk, H, Hk, d, scale, window, sinks,
-                           cu_q, cu_k, total_q, total_k, workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_bwd_window")
+    ws, ws_bytes, workspace = _workspace(workspace, bwd_window_workspace_bytes(B, Nq, Nk, H, Hk, d, window, sinks), device)
+    dq, dk, dv = _out_like("dq", dq, q, device), _out_like("dk", dk, k, device), _out_like("dv", dv, v, device)
+    _launch("fa_bwd_window", device,
+            (*ptrs, *more, lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes, window, sinks, *cu, ws,
+             ws_bytes))
     return dq, dk, dv
 
 
@@ -804,14 +846,14 @@ class KvCache:
 
     def __init__(self, k8, v8, k_scale, v_scale):
         import torch
-        for name, t in (("k8", k8), ("v8", v8)):
-            _check_tensor(name, t, torch.uint8, 4)
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _check_tensor(name, t, torch.float32, 2)
-        self.num_pages, self.Hk, self.page, self.d = k8.shape
-        if v8.shape != k8.shape or k_scale.shape != k8.shape[:2] or v_scale.shape != k8.shape[:2]:
+        self.device = device = _cuda_device("k8", k8)
+        self._codes = _dense("k8", k8, torch.uint8, 4, device), _dense("v8", v8, torch.uint8, 4, device)
+        self._scales = (_dense("k_scale", k_scale, torch.float32, 2, device),
+                        _dense("v_scale", v_scale, torch.float32, 2, device))
+        shape = k8.shape
+        if v8.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
             raise ValueError("codes are [num_pages, Hk, page, d], scales [num_pages, Hk]")
-        _same_device(k8, v8=v8, k_scale=k_scale, v_scale=v_scale)
+        self.num_pages, self.Hk, self.page, self.d = shape
         self.k8, self.v8, self.k_scale, self.v_scale = k8, v8, k_scale, v_scale
 
     @classmethod
@@ -823,44 +865,43 @@ class KvCache:
         return cls(*codes, *scales)
 
 
-def _token_rows(name, t, ndim):
-    """Distance in elements between the token rows of t [B, n, heads, d] or [total, heads, d]."""
+def _token_rows(name, t, ndim, device):
+    """Address of t [B, n, heads, d] or [total, heads, d], and the distance in elements between its
+    token rows."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
-    if t.dim() != ndim:
-        raise ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
-    heads, d = t.shape[-2:]
-    s = t.stride()
+    try:
+        fine = t.dtype is torch.bfloat16 and t.device == device and t.dim() == ndim
+    except AttributeError:
+        fine = False
+    if not fine:
+        _cuda_device(name, t)
+        if t.dtype != torch.bfloat16:
+            raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+        if t.dim() != ndim:
+            raise ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    shape, s = t.shape, t.stride()
+    heads, d = shape[-2:]
     if (d > 1 and s[-1] != 1) or (heads > 1 and s[-2] != d):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     if ndim == 3:
-        return s[0] if t.shape[0] > 1 else heads * d
-    B, n = t.shape[:2]
+        return t.data_ptr(), s[0] if shape[0] > 1 else heads * d
+    B, n = shape[:2]
     if B > 1 and n > 1 and s[0] != n * s[1]:
         raise ValueError("%s: tokens must be evenly spaced" % name)
-    return s[1] if n > 1 else s[0] if B > 1 else heads * d
+    return t.data_ptr(), s[1] if n > 1 else s[0] if B > 1 else heads * d
 
 
-def _lengths(name, t, B, like):
+def _sequences(name, lens, block_table, B, device):
+    """Addresses of the lengths and the table, and the table's width."""
     import torch
-    _check_tensor(name, t, torch.int32, 1)
-    if t.numel() != B:
+    ptr, table = _dense(name, lens, torch.int32, 1, device), _dense("block_table", block_table, torch.int32, 2, device)
+    if lens.shape[0] != B:
         raise ValueError("%s needs %d entries" % (name, B))
-    _same_device(like, **{name: t})
-
-
-def _block_table(t, B, like):
-    import torch
-    _check_tensor("block_table", t, torch.int32, 2)
-    if t.shape[0] != B:
+    rows, width = block_table.shape
+    if rows != B:
         raise ValueError("block_table needs %d rows" % B)
-    _same_device(like, block_table=t)
-    return t.shape[1]
+    return ptr, table, width
 
 
 def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=None, interleaved=False, cu_seqlens=None,
@@ -875,56 +916,59 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
     k's tokens.  Returns the rotated q (q_out or a new contiguous tensor), None
     without q."""
     import torch
+    if stream is not None:
+        with _stream_scope(stream, k):
+            return append_kvcache(cache, k, v, block_table, cache_lens, q, cos, sin, interleaved, cu_seqlens, max_seqlen,
+                                  q_out)
     packed = cu_seqlens is not None
     ndim = 3 if packed else 4
-    k_stride, v_stride = _token_rows("k", k, ndim), _token_rows("v", v, ndim)
-    Hk, d = k.shape[-2:]
-    if v.shape != k.shape or Hk != cache.Hk or d != cache.d:
+    device = cache.device
+    kp, k_stride = _token_rows("k", k, ndim, device)
+    vp, v_stride = _token_rows("v", v, ndim, device)
+    shape = k.shape
+    Hk, d = shape[-2:]
+    if v.shape != shape or Hk != cache.Hk or d != cache.d:
         raise ValueError("k, v and the cache differ in shape")
-    _same_device(cache.k8, k=k, v=v, q=q, cos=cos, sin=sin, q_out=q_out, cu_seqlens=cu_seqlens)
+    cu = None
     if packed:
-        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, 1)
+        cu = _dense("cu_seqlens", cu_seqlens, torch.int32, 1, device)
         if max_seqlen is None:
             raise ValueError("max_seqlen is required with cu_seqlens")
-        B, total, n = cu_seqlens.numel() - 1, k.shape[0], int(max_seqlen)
+        B, total, n = cu_seqlens.shape[0] - 1, shape[0], int(max_seqlen)
     else:
-        B, n = k.shape[:2]
+        B, n = shape[:2]
         total = B * n
-    _lengths("cache_lens", cache_lens, B, k)
-    width = _block_table(block_table, B, k)
+    lens, table, width = _sequences("cache_lens", cache_lens, block_table, B, device)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     rot = max_pos = 0
+    cp = sp = None
     if cos is not None:
-        _check_tensor("cos", cos, torch.float32, 2)
-        _check_tensor("sin", sin, torch.float32, 2)
+        cp, sp = _dense("cos", cos, torch.float32, 2, device), _dense("sin", sin, torch.float32, 2, device)
         if sin.shape != cos.shape:
             raise ValueError("cos and sin differ in shape")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        max_pos, rot = cos.shape
+        rot *= 2
     H = q_stride = 0
+    qp = qop = None
     if q is not None:
-        q_stride = _token_rows("q", q, ndim)
-        if q.shape[:-2] != k.shape[:-2] or q.shape[-1] != d:
+        qp, q_stride = _token_rows("q", q, ndim, device)
+        qs = q.shape
+        if qs[:-2] != shape[:-2] or qs[-1] != d:
             raise ValueError("q and k differ in their tokens")
-        H = q.shape[-2]
+        H = qs[-2]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty(qs, dtype=torch.bfloat16, device=device)
+            qop = q_out.data_ptr()
         else:
-            _check_tensor("q_out", q_out, torch.bfloat16, ndim)
-            if q_out.shape != q.shape:
+            qop = _dense("q_out", q_out, torch.bfloat16, ndim, device)
+            if q_out.shape != qs:
                 raise ValueError("q_out shape mismatch")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with _on_device(k.device):
-        rc = fa_kvcache_append(
-            k.data_ptr(), v.data_ptr(), k_stride, v_stride, q.data_ptr() if q is not None else None, q_stride,
-            q_out.data_ptr() if q is not None else None, cos.data_ptr() if rot else None,
-            sin.data_ptr() if rot else None, max_pos, rot, int(bool(interleaved)), cache.k8.data_ptr(),
-            cache.v8.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), block_table.data_ptr(),
-            cache_lens.data_ptr(), cu_seqlens.data_ptr() if packed else None, B, total, n, H, Hk, d, cache.page,
-            cache.num_pages, width, _stream_handle(stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_kvcache_append")
+    _launch("fa_kvcache_append", device,
+            (kp, vp, k_stride, v_stride, qp, q_stride, qop, cp, sp, max_pos, rot, 1 if interleaved else 0, *cache._codes,
+             *cache._scales, table, lens, cu, B, total, n, H, Hk, d, cache.page, cache.num_pages, width))
     return q_out
 
 
@@ -937,41 +981,38 @@ def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, c
     max_seqlen_k.  causal: query i of n stands at position seq_lens - n + i; window
     (0: none) and sinks as forward_window.  Returns (o like q, lse fp32 [B, H, n])."""
     import torch
+    if stream is not None:
+        with _stream_scope(stream, q):
+            return forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale, causal, window, sinks,
+                                   cu_seqlens_q, max_seqlen_q, workspace, out, lse)
     packed = cu_seqlens_q is not None
-    _check_tensor("q", q, torch.bfloat16, 3 if packed else 4)
-    H, d = q.shape[-2:]
+    device = cache.device
+    qp = _dense("q", q, torch.bfloat16, 3 if packed else 4, device)
+    shape = q.shape
+    H, d = shape[-2:]
     Hk = cache.Hk
     if d != cache.d:
         raise ValueError("q and the cache differ in head dimension")
     if (Hk == 0 and H > 0) or (Hk > 0 and H % Hk):
         raise ValueError("query heads (%d) must be a multiple of key/value heads (%d)" % (H, Hk))
+    cu = None
     if packed:
-        _check_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, 1)
+        cu = _dense("cu_seqlens_q", cu_seqlens_q, torch.int32, 1, device)
         if max_seqlen_q is None:
             raise ValueError("max_seqlen_q is required with cu_seqlens_q")
-        B, n, total = cu_seqlens_q.numel() - 1, int(max_seqlen_q), q.shape[0]
+        B, n, total = cu_seqlens_q.shape[0] - 1, int(max_seqlen_q), shape[0]
     else:
-        B, n = q.shape[:2]
+        B, n = shape[:2]
         total = B * n
-    _same_device(cache.k8, q=q, cu_seqlens_q=cu_seqlens_q)
-    _lengths("seq_lens", seq_lens, B, q)
-    width = _block_table(block_table, B, q)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    causal, window, sinks, max_k = int(bool(causal)), _int32(window), _int32(sinks), int(max_seqlen_k)
-    out = _out_like("out", out, q)
-    lse = _lse_out(lse, (B, H, n), q)
-    with _on_device(q.device):
+    lens, table, width = _sequences("seq_lens", seq_lens, block_table, B, device)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    causal, window, sinks, max_k = 1 if causal else 0, _int32(window), _int32(sinks), int(max_seqlen_k)
+    out = _out_like("out", out, q, device)
+    lse = _lse_out(lse, (B, H, n), device)
+    with _on_device(device):  # the plan depends on the device's SM count
         need = kvcache_workspace_bytes(B, n, max_k, H, Hk, d, causal, window, sinks)
-        if workspace is not None or need > 0:
-            workspace = _workspace(workspace, need, q.device)
-        rc = fa_fwd_kvcache(
-            q.data_ptr(), cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(),
-            cache.v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-            cu_seqlens_q.data_ptr() if packed else None, out.data_ptr(), lse.data_ptr(), B, total, n, max_k, H, Hk, d,
-            cache.page, cache.num_pages, width, float(scale), causal, window, sinks,
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream_handle(stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_fwd_kvcache")
+    ws, ws_bytes, workspace = _workspace(workspace, need, device)
+    _launch("fa_fwd_kvcache", device,
+            (qp, *cache._codes, *cache._scales, table, lens, cu, out.data_ptr(), lse.data_ptr(), B, total, n, max_k, H, Hk,
+             d, cache.page, cache.num_pages, width, scale, causal, window, sinks, ws, ws_bytes))
     return out, lse

@@ -453,9 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // from k0 on, and up to k1 - 1 unless kj is a sink.
             const int k0 = key_ok ? kj - q_pos - hh * 32 : 32;
             const int k1 = kj < p.sinks ? 32 : kj + p.window - q_pos - hh * 32;
+            const uint32_t seen = bits_below(k1) & ~bits_below(k0);
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (k < k0 || k >= k1) e[k] = 0.f;
+              if ((seen & (1u << k)) == 0u) e[k] = 0.f;
           }
 #pragma unroll
           for (int k = 0; k < 32; k += 2) pk[16 * hh + k / 2] = ptx::pack_bf16x2(e[k], e[k + 1]);

@@ -43,6 +43,9 @@ __host__ __device__ __forceinline__ bool win_sees(int kt, int lo, int hi, int ns
   return kt <= hi && (kt < nsk || kt >= lo);
 }
 
+// The low n bits set (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
+
 struct WinUnit {
   int b, h, hk;
   int q_start, q_end, k_start, k_end;
@@ -89,7 +92,9 @@ struct WinParams {
 template <int BC, bool VARLEN, bool KPAD>
 __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
   WinUnit w;
-  const int mb = u % p.num_mblocks;
+  // Packed batches: last query blocks first (under a long window the longest
+  // units), so that the running CTAs even out at the end.
+  const int mb = VARLEN ? p.num_mblocks - 1 - u % p.num_mblocks : u % p.num_mblocks;
   const int r = u / p.num_mblocks;
   w.h = r % p.H;
   w.b = r / p.H;
@@ -449,22 +454,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool border = kw.lo != 0 || kw.hi != BC || kbase + BC - 1 > pos_first ||
                             (kbase <= pos_last - p.window && kbase + BC > p.sinks);
         float s[BC];
-        auto mask = [&](int c0, int c1) {
-          const int hi = min(kw.hi - 1, pos - kbase);  // last visible column
-          const int lo = pos - p.window - kbase;       // columns up to here are behind the window
-          const int snk = p.sinks - kbase;             // columns before here are sinks
+        // Border tiles: the row's visible columns as 32-bit words, [a, e) (window
+        // and diagonal) and [kw.lo, f) (sinks): a bit test and a select per score
+        // (four comparisons per score made a border tile cost several others).
+        uint32_t seen[BC / 32];
+        auto find_seen = [&]() {
+          const int e = min(kw.hi, pos - kbase + 1);
+          const int a = max(kw.lo, pos - p.window - kbase + 1);
+          const int f = min(e, p.sinks - kbase);
 #pragma unroll
-          for (int c = 0; c < BC; ++c)
-            if (c >= c0 && c < c1 && (c < kw.lo || c > hi || (c <= lo && c >= snk))) s[c] = -INFINITY;
-        };
-        auto load_scores = [&]() {
-          uint32_t sr[BC];
-#pragma unroll
-          for (int c = 0; c < BC / 32; ++c) ptx::tmem_ld32(tS + c * 32, &sr[c * 32]);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < BC; ++c) s[c] = __uint_as_float(sr[c]);
-          if (border) mask(0, BC);
+          for (int c = 0; c < BC / 32; ++c)
+            seen[c] = border ? (bits_below(e - 32 * c) & ~bits_below(a - 32 * c)) |
+                                   (bits_below(f - 32 * c) & ~bits_below(kw.lo - 32 * c))
+                             : ~0u;
         };
         uint32_t pk[BC / 2];
         auto exp_range = [&](int c0, int c1, float ng, uint64_t (&acc)[4]) {
@@ -489,11 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // The speculative maximum of fa_fwd_kernel: exponentials against the
         // current reference first; a block sum of at most 2^T proves that the
-        // rescale rule leaves the reference in place.
+        // rescale rule leaves the reference in place.  Tiles with a border, and
+        // a row's first, go another way below.
         float alpha = 1.f, lblk = 0.f;
-        bool slow = __all_sync(0xffffffffu, m_ref == -INFINITY);
-        const float ng_ref = m_ref == -INFINITY ? 0.f : -m_ref * c2;
-        if (!slow && !border) {
+        bool slow = border || __all_sync(0xffffffffu, m_ref == -INFINITY);
+        if (!slow) {
+          const float ng_ref = m_ref == -INFINITY ? 0.f : -m_ref * c2;
           uint32_t sr[BC];
 #pragma unroll
           for (int c = 0; c < BC / 64; ++c) ptx::tmem_ld32(tS + c * 32, &sr[c * 32]);
@@ -510,18 +513,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           exp_range(BC / 2, BC, ng_ref, acc);
           lblk = sum_acc(acc);
           slow = __any_sync(0xffffffffu, m_ref == -INFINITY || !(lblk <= accept_sum));
-          if (slow) load_scores();  // the scores were consumed
-        } else {
-          load_scores();
-          if (!slow) {
-            uint64_t acc[4] = {0, 0, 0, 0};
-            exp_range(0, BC, ng_ref, acc);
-            lblk = sum_acc(acc);
-            slow = __any_sync(0xffffffffu, m_ref == -INFINITY || !(lblk <= accept_sum));
-            if (slow) load_scores();
-          }
         }
         if (slow) {
+          {
+            uint32_t sr[BC];
+#pragma unroll
+            for (int c = 0; c < BC / 32; ++c) ptx::tmem_ld32(tS + c * 32, &sr[c * 32]);
+            find_seen();
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < BC; ++c) s[c] = __uint_as_float(sr[c]);
+          }
+          if (border) {
+#pragma unroll
+            for (int c = 0; c < BC; ++c)
+              if ((seen[c / 32] & (1u << (c % 32))) == 0u) s[c] = -INFINITY;
+          }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int c = 4; c < BC; c += 8) {
@@ -537,8 +544,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (bm > m_ref && (m_ref == -INFINITY || (bm - m_ref) * c2 > p.rescale_threshold)) m_new = bm;
           alpha = (m_new == m_ref) ? 1.f : ptx::ex2((m_ref - m_new) * c2);
           m_ref = m_new;
+          const float ng = m_ref == -INFINITY ? 0.f : -m_ref * c2;
           uint64_t acc[4] = {0, 0, 0, 0};
-          exp_range(0, BC, m_ref == -INFINITY ? 0.f : -m_ref * c2, acc);
+          exp_range(0, BC, ng, acc);
           lblk = sum_acc(acc);
         }
 #pragma unroll

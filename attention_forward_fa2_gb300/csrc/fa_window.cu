@@ -128,7 +128,12 @@ int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v,
   p.window = std::min(p.window, std::max(p.Nk, 1));
   p.sinks = std::min(p.sinks, p.Nk);
   p.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-  p.rescale_threshold = 8.f;
+  // A row's first tile may show it a single key (the window's start, few sinks),
+  // so its reference maximum is often far below its true one.  Nothing is lost
+  // by that: weights are bf16 and sums fp32, whose relative precision does not
+  // depend on the reference, and 2^40 is far from overflow; a threshold of 2^8
+  // would send most rows' second tile through the slow path.
+  p.rescale_threshold = 40.f;
   const cudaError_t ce = d == 128 ? dispatch_win<128>(a, varlen, kpad) : dispatch_win<64>(a, varlen, kpad);
   return ce == cudaSuccess ? FA_OK : host_cuda_fail(ce);
 }

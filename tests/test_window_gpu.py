@@ -80,7 +80,12 @@ def test_full_window_is_the_causal_forward():
     o, lse = fa.forward_window(q, k, v, 1 << 40)
     oc, lsec = fa.forward_qk(q, k, v, causal=True)
     _ok()
-    assert torch.equal(o, oc) and torch.equal(lse, lsec)
+    # Both are roundings of the same values, each within `bound` of them, and so at most
+    # twice that apart (the two kernels take their reference maxima by different rules).
+    for b in range(2):
+        _, _, bound = R.forward(q[b], k[b], v[b], 128 ** -0.5, R.visible(300, 450, 0, 0, device="cuda"))
+        R.check(o[b], oc[b].double(), 2 * bound, "o[%d]" % b)
+    assert (lse - lsec).abs().max().item() <= 2 * R.LSE_TOL
 
 
 LENS = [(0, 0), (1, 1), (127, 127), (0, 40), (128, 300), (129, 129), (77, 0), (513, 513), (300, 100)]
