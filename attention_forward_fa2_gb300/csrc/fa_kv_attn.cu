@@ -15,46 +15,37 @@
 namespace fa {
 namespace {
 
-constexpr int kMaxKvSplits = 256;
-
-// Query rows per key/value head (queries times heads of a group) up to which
-// the split kernel runs; above, the query chunk is long enough for 128-row
-// tcgen05 tiles.
+// Query rows per key/value head (queries times heads of a group) up to which the
+// kernel for few rows runs, a unit of 16 rows at a time (the codes of later row
+// groups come from L2); above, the query chunk is long enough for 128-row tcgen05
+// tiles.
 constexpr int kFewRows = 64;
 
 struct KvPlan {
   bool few;
-  int mt, row_groups, splits, split_steps;
+  int ctas;             // few rows: CTAs (at most three an SM; fewer when there are fewer steps)
   int k_pad;            // chunk form: key rows per sequence of the bf16 copy
   size_t ws_bytes;
 };
 
-// Depends on the sizes alone.  The splits give every SM about four CTAs of two
-// resident ones (ragged batches even out), each at least one step of 128 keys.
+// Depends on the sizes alone.
 KvPlan kv_plan(int B, int max_q, int max_k, int H, int Hk, int d, int causal, int window, int sinks, int num_sms) {
   KvPlan z{};
-  const int G = Hk > 0 ? H / Hk : 1;
-  const long long rows = static_cast<long long>(max_q) * G;
+  const long long rows = static_cast<long long>(max_q) * (Hk > 0 ? H / Hk : 1);
   z.few = rows <= kFewRows;
   if (!z.few) {
     z.k_pad = (max_k + kKvTile - 1) / kKvTile * kKvTile;
     z.ws_bytes = 2 * static_cast<size_t>(B) * z.k_pad * Hk * d * 2;
     return z;
   }
-  z.mt = rows <= 16 ? 1 : 2;
-  z.row_groups = static_cast<int>((rows + 16 * z.mt - 1) / (16 * z.mt));
   long long steps = (static_cast<long long>(max_k) + kKvTile - 1) / kKvTile;
   if (causal && window > 0) {
     const long long win = (static_cast<long long>(window) + max_q + kKvTile - 2) / kKvTile + 1;
     steps = std::min(steps, win + (static_cast<long long>(sinks) + kKvTile - 1) / kKvTile);
   }
-  steps = std::max<long long>(steps, 1);
-  const long long units = std::max<long long>(static_cast<long long>(B) * Hk * z.row_groups, 1);
-  long long splits = std::min<long long>((8LL * num_sms + units - 1) / units, kMaxKvSplits);
-  splits = std::max<long long>(1, std::min(splits, steps));
-  z.split_steps = static_cast<int>((steps + splits - 1) / splits);
-  z.splits = static_cast<int>((steps + z.split_steps - 1) / z.split_steps);
-  if (z.splits > 1) z.ws_bytes = static_cast<size_t>(z.splits) * B * H * max_q * (static_cast<size_t>(d) + 1) * 4;
+  const long long all = B * static_cast<long long>(Hk) * ((rows + kKvRows - 1) / kKvRows) * std::max<long long>(steps, 1);
+  z.ctas = static_cast<int>(std::max<long long>(1, std::min<long long>(all, kKvCtasPerSm * num_sms)));
+  z.ws_bytes = static_cast<size_t>(z.ctas) * (16 + 2 * kKvRows * (static_cast<size_t>(d) + 1) * 4);
   return z;
 }
 
@@ -67,19 +58,16 @@ int encode_cache(CUtensorMap* m, const void* codes, long long rows, int d, int p
                      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <int D, int MT>
-cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const KvAttnParams& p, cudaStream_t stream) {
-  auto* kern = &fa_kv_attn_kernel<D, MT>;
-  constexpr int smem = KvSmem<D, MT>::kAlloc;
+template <int D>
+cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const KvAttnParams& p, int ctas, cudaStream_t stream) {
+  auto* kern = &fa_kv_attn_kernel<D>;
+  constexpr int smem = KvSmem<D>::kAlloc;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.splits, p.Hk * p.row_groups, p.B);
-  kern<<<grid, kKvThreads, smem, stream>>>(tk, tv, p);
-  if (p.splits > 1) {
-    const long long rows = static_cast<long long>(p.B) * p.H * p.max_q;
-    fa_kv_join_kernel<D, 16 * MT><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
-  }
+  kern<<<ctas, kKvThreads, smem, stream>>>(tk, tv, p);
+  const dim3 grid(ctas, std::min(kKvRows, p.max_q * p.G));
+  fa_kv_join_kernel<D><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -233,13 +221,10 @@ int fa_fwd_kvcache(const void* q, const void* k8, const void* v8, const float* k
     p.causal = causal != 0;
     p.window = win;
     p.sinks = snk;
-    p.row_groups = z.row_groups;
-    p.splits = z.splits;
-    p.split_steps = z.split_steps;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    if (static_cast<long long>(Hk) * z.row_groups > 65535) return FA_ERR_INVALID_ARG;
-    p.ws_o = static_cast<float*>(workspace);
-    p.ws_lse = p.ws_o + static_cast<size_t>(z.splits) * B * H * max_seqlen_q * d;
+    p.cut = static_cast<int4*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(p.cut + z.ctas);
+    p.part_o = p.part_lse + static_cast<size_t>(z.ctas) * 2 * fa::kKvRows;
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
     CUtensorMap tk, tv;
@@ -247,10 +232,7 @@ int fa_fwd_kvcache(const void* q, const void* k8, const void* v8, const float* k
     const long long rows = std::max<long long>(static_cast<long long>(num_pages) * Hk * page, page);
     if ((rc = fa::encode_cache(&tk, num_pages > 0 ? k8 : q, rows, d, page)) != FA_OK) return rc;
     if ((rc = fa::encode_cache(&tv, num_pages > 0 ? v8 : q, rows, d, page)) != FA_OK) return rc;
-    if (d == 128)
-      e = z.mt == 1 ? fa::launch_few<128, 1>(tk, tv, p, st) : fa::launch_few<128, 2>(tk, tv, p, st);
-    else
-      e = z.mt == 1 ? fa::launch_few<64, 1>(tk, tv, p, st) : fa::launch_few<64, 2>(tk, tv, p, st);
+    e = d == 128 ? fa::launch_few<128>(tk, tv, p, z.ctas, st) : fa::launch_few<64>(tk, tv, p, z.ctas, st);
     return e == cudaSuccess ? FA_OK : fa::host_cuda_fail(e);
   }
   fa::DequantParams dq{};

@@ -5,17 +5,23 @@
 //     s_j = scale * ks(page j) * q_i . K8_j        over the keys j <= p in sight
 //     o_i = sum_j softmax_j(s_j) * vs(page j) * V8_j,   lse_i = log sum_j e^{s_j}.
 // Bound by reading the codes once, 2 d bytes per key and key/value head: the
-// G = H / Hk query heads (times n_q rows) that share them run in one CTA, and long
-// sequences are cut over keys (splits) so that every SM reads; a second kernel
-// joins the splits ("GPU 内核与 FlashAttention" §11.2).
+// G = H / Hk query heads (times n_q rows) that share them are computed together,
+// 16 rows to a unit of work (sequence, key/value head, row group).
 //
-// A CTA holds up to 16 * MT query rows, and walks key tiles of 128 tokens through
-// a ring in shared memory that one warp fills by TMA, a page at a time (each lane
-// looks up and loads one page of the tile).  Four warps compute, 32 tokens of
-// every tile each, with an online softmax of their own; they meet once at the end.
-//   Products: mma.sync m16n8k16 in f16 with fp32 sums.  With at most 32 rows the
-//   tensor work is 1/8 to 1/4 of a 128-row tcgen05 tile and hides behind the
-//   loads; operands come from registers, which is where e4m3 codes become f16
+// Schedule: the steps (key tiles of 128 tokens) of all units, laid end to end,
+// are cut into equal ranges, one per resident CTA, so that every SM reads the
+// same number of bytes whatever the lengths.  A CTA finds its range by a scan of
+// the lengths, computes the units that lie in it whole, and leaves the ones cut
+// by its borders in fp32 in the workspace (at most two); a second kernel joins
+// them ("GPU 内核与 FlashAttention" §11.2).
+//
+// A CTA: warp 4 walks the range ahead of the others, fills a ring of key tiles by
+// TMA, a page at a time (each lane looks up and loads one page of the tile), and
+// lays out the next unit's queries; warps 0-3 compute, 32 tokens of every tile
+// each, with an online softmax of their own, and meet at the end of a unit.
+//   Products: mma.sync m16n8k16 in f16 with fp32 sums.  With 16 rows the
+//   tensor work is 1/8 of a 128-row tcgen05 tile and hides behind the loads;
+//   operands come from registers, which is where e4m3 codes become f16
 //   (exact: f16 holds every e4m3 value).  q is scaled per row by a power of two
 //   to below 2^8, so that f16 holds its bf16 values exactly down to 2^-22 of the
 //   row's largest; P is rounded to f16 (2^-11, finer than bf16).
@@ -28,6 +34,9 @@
 //   k-steps (a permutation of d that q's fragments share), and V through
 //   ldmatrix.trans on byte pairs, one byte permute apart from the B fragment;
 //   perm() places the two rows that a quarter-warp reads in different banks.
+//   Occupancy: three CTAs an SM (128 registers, so q's fragments live in shared
+//   memory): a warp's step is one dependent chain of loads, products, shuffles
+//   and exponentials, and other warps have to cover it.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -39,6 +48,10 @@
 
 namespace fa {
 
+constexpr int kKvRows = 16;       // query rows per unit
+constexpr int kKvThreads = 160;   // warps 0-3 compute, warp 4 loads
+constexpr int kKvCtasPerSm = 3;
+
 struct KvAttnParams {
   const __nv_bfloat16* q;   // [total_q, H, d], or [B, max_q, H, d] (cu null)
   __nv_bfloat16* o;         // like q
@@ -48,65 +61,77 @@ struct KvAttnParams {
   int B, max_q, max_k, total_q, H, Hk, G;
   int width, page, num_pages;
   int causal, window, sinks;
-  int row_groups;           // CTAs of 16 * MT rows per (sequence, key/value head)
-  int splits, split_steps;  // key splits, steps per split
   float scale_log2;
-  float *ws_o, *ws_lse;     // [splits, B, H, max_q, d] and [splits, B, H, max_q] (log2 units)
+  // Workspace: a unit cut by the borders of CTA c's range is at place 2c (begun by
+  // an earlier CTA) or 2c + 1 (begun by c, ended later); cut[c] names the unit
+  // that ends in c and was begun by an earlier CTA.
+  int4* cut;                // [ctas]: b (-1: none), key/value head, first row, CTA that began it
+  float* part_o;            // [2 ctas, 16, d] normalised
+  float* part_lse;          // [2 ctas, 16], log2 units
   unsigned long long timeout_ns;
   int* status;
 };
 
-constexpr int kKvThreads = 160;  // warps 0-3 compute, warp 4 loads
+enum KvSite : int { kKvSiteLoad = 201, kKvSiteLoadQ = 202, kKvSiteCompute = 203, kKvSiteComputeQ = 204, kKvSiteMeet = 205 };
 
-enum KvSite : int { kKvSiteLoad = 201, kKvSiteCompute = 202 };
+// A unit of work as warp 4 hands it to the others.
+struct KvUnit {
+  int b;               // -1: no more units
+  int hk, r0, rows;    // key/value head, first row, rows of the sequence (n_q * G)
+  int row0, n_q, len;  // first packed query row, queries, keys
+  int steps;           // steps of this CTA
+  int ns, gap, t0;     // key tile of step t: t < ns ? t : t + gap, from t0
+  int place;           // -1: whole (write o and lse), else place in the workspace
+};
 
-template <int D, int MT>
+template <int D>
 struct KvSmem {
-  static constexpr int kStages = D == 128 ? (MT > 1 ? 6 : 3) : 6;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kTileBytes = kKvTile * D;
-  static constexpr int kStageBytes = 2 * kTileBytes;  // K then V
-  static constexpr int kRowStride = D + 16;           // floats; rows of a quarter-warp in different banks
-  static constexpr int kOffConst = kStages * kStageBytes;         // per stage and page: coefficient, log2 vs, 1 / vs
+  static constexpr int kStageBytes = 2 * kTileBytes;               // K then V
+  static constexpr int kOffConst = kStages * kStageBytes;          // per stage and page: ks, log2 vs, 1 / vs
   static constexpr int kConstBytes = 3 * (kKvTile / 16) * 4;
-  static constexpr int kOffQ = kOffConst + kStages * kConstBytes;  // q fragments (MT > 1)
-  static constexpr int kQBytes = MT > 1 ? MT * (D / 16) * 32 * 16 : 0;
-  static constexpr int kOffBar = kOffQ + kQBytes;
-  static constexpr int kOffAbort = kOffBar + 2 * kStages * 8;
-  static constexpr int kBytes = kOffAbort + 16;
+  static constexpr int kOffQ = kOffConst + kStages * kConstBytes;  // two units' q as A fragments
+  static constexpr int kQBytes = (D / 16) * 32 * 16;
+  static constexpr int kOffCoef = kOffQ + 2 * kQBytes;             // and the factor of each row's scores
+  static constexpr int kOffUnit = kOffCoef + 2 * kKvRows * 4;
+  static constexpr int kUnitBytes = 64;
+  static constexpr int kOffBar = kOffUnit + 2 * kUnitBytes;
+  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int kOffScan = kOffBar + kNumBars * 8;          // 6 long long, 2 long long, abort
+  static constexpr int kBytes = kOffScan + 80;
   static constexpr int kAlloc = kBytes + 1024;
-  // The join at the end reuses the ring: per warp and row m, l and d floats.
-  static_assert(4 * 16 * MT * (kRowStride + 2) * 4 <= kStages * kStageBytes, "join area");
-  static_assert(kOffQ % 16 == 0 && kOffBar % 8 == 0, "alignment");
+  // At the end of a unit its last stage takes two warps' rows: d floats, m and l.
+  static constexpr int kRowStride = D + 16;                        // floats; rows of a quarter-warp in different banks
+  static_assert(2 * kKvRows * (kRowStride + 2) * 4 <= kStageBytes, "join area");
+  static_assert(sizeof(KvUnit) <= kUnitBytes && kOffQ % 16 == 0 && kOffBar % 8 == 0, "layout");
+  static_assert(kKvCtasPerSm * (kAlloc + 1024) <= 233472, "three CTAs an SM");
 };
 
-// The query rows and key range of one CTA.
-struct KvWork {
-  int row0;            // first packed query row of the sequence
-  int n_q, len;
-  int rows;            // rows of this key/value head: n_q * G, row r is query r / G, head r % G
-  int r0, r1;          // rows of this group
+// The queries and keys of a sequence, and the key tiles its rows see.
+struct KvSeq {
+  int row0, n_q, len, rows;
   KvRange range;
-  int p_min, p_max;
+  int units_per_head;  // row groups
   bool bad;
+  // Steps of a unit: a sequence without keys takes one, in which it sees nothing.
+  __device__ __forceinline__ int steps() const { return range.steps > 0 ? range.steps : 1; }
 };
-template <int RG>
-__device__ __forceinline__ KvWork kv_work(const KvAttnParams& p, int b, int rg) {
-  KvWork w;
-  w.row0 = p.cu ? p.cu[b] : b * p.max_q;
-  w.n_q = p.cu ? p.cu[b + 1] - w.row0 : p.max_q;
-  w.len = p.lens[b];
-  w.bad = w.n_q < 0 || w.n_q > p.max_q || w.row0 < 0 || w.row0 > p.total_q - w.n_q || w.len < 0 || w.len > p.max_k ||
-          w.len > static_cast<long long>(p.width) * p.page;
-  if (w.bad) w.n_q = 0;
-  w.rows = w.n_q * p.G;
-  w.r0 = rg * RG;
-  w.r1 = min(w.rows, w.r0 + RG);
-  const int i0 = w.r0 / p.G, i1 = (w.r1 - 1) / p.G;
-  w.p_min = p.causal ? i0 + w.len - w.n_q : w.len - 1;
-  w.p_max = p.causal ? i1 + w.len - w.n_q : w.len - 1;
-  w.range = kv_range(w.p_min, w.p_max, p.window, p.sinks);
-  if (w.r0 >= w.rows) w.range.steps = 0;
-  return w;
+__device__ __forceinline__ KvSeq kv_seq(const KvAttnParams& p, int b) {
+  KvSeq s;
+  s.row0 = p.cu ? p.cu[b] : b * p.max_q;
+  s.n_q = p.cu ? p.cu[b + 1] - s.row0 : p.max_q;
+  s.len = p.lens[b];
+  s.bad = s.n_q < 0 || s.n_q > p.max_q || s.row0 < 0 || s.row0 > p.total_q - s.n_q || s.len < 0 || s.len > p.max_k ||
+          s.len > static_cast<long long>(p.width) * p.page;
+  if (s.bad) s.n_q = 0;
+  s.rows = s.n_q * p.G;
+  s.units_per_head = (s.rows + kKvRows - 1) / kKvRows;
+  s.range = kv_range(p.causal ? s.len - s.n_q : s.len - 1, s.len - 1, p.window, p.sinks);
+  return s;
+}
+__device__ __forceinline__ long long kv_flat(const KvAttnParams& p, const KvSeq& s) {
+  return static_cast<long long>(s.steps()) * s.units_per_head * p.Hk;
 }
 
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
@@ -167,187 +192,285 @@ __device__ __forceinline__ int kv_perm(int n) {
   return D == 128 ? (n >> 1) + ((n & 1) << 2) : n;
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kKvThreads, D == 128 && MT > 1 ? 1 : 2)
+template <int D>
+__global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
     fa_kv_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const KvAttnParams p) {
-  using L = KvSmem<D, MT>;
-  constexpr int RG = 16 * MT;
+  using L = KvSmem<D>;
   constexpr int kSteps = D / 16;  // k-steps of S
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw_base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x;
-  const int hk = blockIdx.y / p.row_groups, rg = blockIdx.y % p.row_groups;
-  const int b = blockIdx.z;
-
-  const KvWork w = kv_work<RG>(p, b, rg);
-  if (w.bad && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(p.status, kErrBadSeqlens, 0);
-  if (w.r0 >= w.rows) return;
-  const int t0 = split * p.split_steps;
-  const int t1 = min(w.range.steps, t0 + p.split_steps);
-  if (t0 >= t1 && p.splits > 1) return;  // the join knows which splits hold keys
+  const int n = lane >> 2, c = lane & 3;
 
   auto full = [&](int s) -> uint32_t { return base + L::kOffBar + 8u * s; };
   auto empty = [&](int s) -> uint32_t { return base + L::kOffBar + 8u * (L::kStages + s); };
-  volatile int* const s_abort = reinterpret_cast<volatile int*>(gbase + L::kOffAbort);
+  auto q_full = [&](int s) -> uint32_t { return base + L::kOffBar + 8u * (2 * L::kStages + s); };
+  auto q_empty = [&](int s) -> uint32_t { return base + L::kOffBar + 8u * (2 * L::kStages + 2 + s); };
+  const uint32_t meet_bar = base + L::kOffBar + 8u * (2 * L::kStages + 4);
+  long long* const s_scan = reinterpret_cast<long long*>(gbase + L::kOffScan);  // warp sums, then (sequence, its first step)
+  volatile int* const s_abort = reinterpret_cast<volatile int*>(gbase + L::kOffScan + 64);
   if (threadIdx.x == 0) {
     *s_abort = 0;
     for (int s = 0; s < L::kStages; ++s) {
       ptx::mbar_init(full(s), 32);
       ptx::mbar_init(empty(s), 4);
     }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(q_full(s), 32);
+      ptx::mbar_init(q_empty(s), 4);
+    }
+    ptx::mbar_init(meet_bar, 4);
     ptx::fence_mbar_init();
+  }
+  // ------------------------------------------ this CTA's range of the steps of all units
+  const int per = (p.B + kKvThreads - 1) / kKvThreads;  // sequences of a thread
+  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const KvSeq s = kv_seq(p, b);
+    if (s.bad && blockIdx.x == 0) record_error(p.status, kErrBadSeqlens, 0);
+    mine += kv_flat(p, s);
+  }
+  long long pre = mine;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, pre, k);
+    if (lane >= k) pre += v;
+  }
+  if (lane == 31) s_scan[warp] = pre;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kKvThreads / 32; ++w) {
+    if (w < warp) pre += s_scan[w];
+    total += s_scan[w];
+  }
+  pre -= mine;  // steps before this thread's sequences
+  const long long span = (total + gridDim.x - 1) / gridDim.x;
+  const long long begin = blockIdx.x * span, end = min(total, begin + span);
+  if (threadIdx.x == 0 && p.cut != nullptr) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (begin >= end) return;  // the whole CTA
+  if (begin >= pre && begin < pre + mine) {
+    long long at = pre;
+    int b = b0;
+    for (; b < b1; ++b) {
+      const long long f = kv_flat(p, kv_seq(p, b));
+      if (begin < at + f) break;
+      at += f;
+    }
+    s_scan[6] = b;
+    s_scan[7] = at;
   }
   __syncthreads();
 
-  const int n = lane >> 2, c = lane & 3;
-  float m[MT][2], l[MT][2];
-  float acc[MT][kSteps][2][4];  // [chunk of 16 d][even / odd d][C fragment]
+  if (warp == 4) {
+    // ================================================================ loads
+    int b = static_cast<int>(s_scan[6]);
+    long long at = s_scan[7];  // first step of sequence b
+    long long pos = begin;
+    const int ppt = kKvTile / p.page;  // pages per tile: one per lane
+    int done = 0, units = 0;
+    bool ok = true;
+    while (ok && pos < end) {
+      KvSeq s = kv_seq(p, b);
+      while (pos >= at + kv_flat(p, s)) {
+        at += kv_flat(p, s);
+        s = kv_seq(p, ++b);
+      }
+      const int steps = s.steps();
+      const long long local = pos - at;
+      const int unit = static_cast<int>(local / steps), t0 = static_cast<int>(local - static_cast<long long>(unit) * steps);
+      const int t1 = static_cast<int>(min(static_cast<long long>(steps), t0 + (end - pos)));
+      const int hk = unit / s.units_per_head, r0 = (unit % s.units_per_head) * kKvRows;
+      // ---- the unit and its queries, as A fragments: k-step kk = 4 h + wd takes
+      // d = 16 (c + 4 h) + 4 wd + {0, 1 | 2, 3} of rows n and n + 8.
+      const int us = units & 1;
+      if (!ptx::mbar_wait_warp(q_empty(us), ((units >> 1) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
+        if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteLoadQ);
+        break;
+      }
+      if (lane == 0) {
+        KvUnit* const u = reinterpret_cast<KvUnit*>(gbase + L::kOffUnit + us * L::kUnitBytes);
+        u->b = b;
+        u->hk = hk;
+        u->r0 = r0;
+        u->rows = s.rows;
+        u->row0 = s.row0;
+        u->n_q = s.n_q;
+        u->len = s.len;
+        u->steps = t1 - t0;
+        u->ns = s.range.ns;
+        u->gap = s.range.gap;
+        u->t0 = t0;
+        u->place = t0 > 0 ? 2 * blockIdx.x : t1 < steps ? 2 * blockIdx.x + 1 : -1;
+        if (t0 > 0 && t1 == steps)
+          p.cut[blockIdx.x] = make_int4(b, hk, r0, static_cast<int>((pos - t0) / span));
+      }
+      {
+        float* const coef = reinterpret_cast<float*>(gbase + L::kOffCoef) + us * kKvRows;
+        uint32_t frag[kSteps][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 8 * e + n;
+          const bool in = r < s.rows;
+          const __nv_bfloat16* src =
+              p.q + (static_cast<size_t>(s.row0 + (in ? r / p.G : 0)) * p.H + hk * p.G + (in ? r % p.G : 0)) * D;
+          uint4 raw[D / 64][2];
+          uint32_t amax = 0;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              raw[h][v] = make_uint4(0, 0, 0, 0);
+              if (in) raw[h][v] = *reinterpret_cast<const uint4*>(src + 16 * (c + 4 * h) + 8 * v);
+            }
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const uint32_t wd[4] = {raw[h][v].x, raw[h][v].y, raw[h][v].z, raw[h][v].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) amax = max(amax, max((wd[k] << 16) & 0x7fffffffu, wd[k] & 0x7fff0000u));
+            }
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // Exponent that brings the row's largest magnitude to [2^7, 2^8).
+          const int ex = min(max(static_cast<int>(amax >> 23) - 127 - 7, -119), 119);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          if (c == 0) coef[8 * e + n] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * p.scale_log2;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const uint32_t wd[4] = {raw[h][v].x, raw[h][v].y, raw[h][v].z, raw[h][v].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                frag[4 * h + 2 * v + (k >> 1)][2 * (k & 1) + e] =
+                    pack_f16x2(__uint_as_float(wd[k] << 16) * down, __uint_as_float(wd[k] & 0xffff0000u) * down);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          ptx::st_shared_v4(base + L::kOffQ + us * L::kQBytes + (k * 32 + lane) * 16, frag[k][0], frag[k][1], frag[k][2],
+                            frag[k][3]);
+      }
+      ptx::mbar_arrive(q_full(us));
+      ++units;
+      // ---- the unit's key tiles
+      auto page_of = [&](int t) -> int {  // this lane's page of step t; -1: nothing to load
+        if (t >= t1 || lane >= ppt) return -1;
+        const int a = (t < s.range.ns ? t : t + s.range.gap) * kKvTile + lane * p.page;
+        if (!kv_needed(s.range, a, p.page)) return -1;
+        const int id = p.table[static_cast<size_t>(b) * p.width + a / p.page];
+        if (kv_page_ok(id, p.num_pages)) return id;
+        record_error(p.status, kErrBadPage, 0);
+        return -1;
+      };
+      int next = page_of(t0);
+      for (int t = t0; t < t1; ++t, ++done) {
+        const int st = done % L::kStages;
+        const int id = next;
+        next = page_of(t + 1);
+        const size_t ph = static_cast<size_t>(id < 0 ? 0 : id) * p.Hk + hk;
+        float ks = 0.f, vs = 1.f;
+        if (id >= 0) {
+          ks = p.k_scale[ph];
+          vs = p.v_scale[ph];
+        }
+        if (!ptx::mbar_wait_warp(empty(st), ((done / L::kStages) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
+          if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteLoad);
+          ok = false;
+          break;
+        }
+        if (id >= 0) {
+          mbar_expect_tx(full(st), 2 * p.page * D);
+          const uint32_t dst = base + st * L::kStageBytes + lane * p.page * D;
+          const int row = static_cast<int>(ph) * p.page;
+          tma_load_2d(dst, &tm_k, full(st), 0, row);
+          tma_load_2d(dst + L::kTileBytes, &tm_v, full(st), 0, row);
+        }
+        if (lane < ppt) {
+          float* const cst = reinterpret_cast<float*>(gbase + L::kOffConst + st * L::kConstBytes) + 3 * lane;
+          cst[0] = ks;
+          cst[1] = log2f(vs);
+          cst[2] = 1.f / vs;
+        }
+        ptx::mbar_arrive(full(st));
+      }
+      pos += t1 - t0;
+    }
+    // The end of the units.
+    if (ok && ptx::mbar_wait_warp(q_empty(units & 1), ((units >> 1) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
+      if (lane == 0) reinterpret_cast<KvUnit*>(gbase + L::kOffUnit + (units & 1) * L::kUnitBytes)->b = -1;
+      ptx::mbar_arrive(q_full(units & 1));
+    }
+    // Nothing may land in shared memory after the CTA is gone.
+    for (int s = 0; s < L::kStages; ++s)
+      if (done > s) ptx::mbar_wait_drain(full(s), ((done - 1 - s) / L::kStages) & 1u, p.timeout_ns);
+    return;
+  }
+
+  // ================================================================ compute
+  const int page_shift = 31 - __clz(p.page);
+  int done = 0;
+  // The four warps wait for one another (bounded like every wait: a warp that gave
+  // up never comes, and bar.sync would wait for it for ever).
+  uint32_t met = 0;
+  auto meet = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(meet_bar);
+    const bool all = ptx::mbar_wait_warp(meet_bar, met & 1u, s_abort, p.timeout_ns);
+    ++met;
+    if (!all && lane == 0) record_error(p.status, kErrTimeout, kKvSiteMeet);
+    return all;
+  };
+#pragma unroll 1
+  for (int units = 0;; ++units) {
+    const int us = units & 1;
+    if (!ptx::mbar_wait_warp(q_full(us), (units >> 1) & 1u, s_abort, p.timeout_ns)) {
+      if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteComputeQ);
+      return;
+    }
+    const KvUnit w = *reinterpret_cast<const KvUnit*>(gbase + L::kOffUnit + us * L::kUnitBytes);
+    if (w.b < 0) return;
+    const uint32_t qf = base + L::kOffQ + us * L::kQBytes + lane * 16;
+    const float* const s_coef = reinterpret_cast<const float*>(gbase + L::kOffCoef) + us * kKvRows;
+    const float coef[2] = {s_coef[n], s_coef[8 + n]};
+    const int off = w.len - w.n_q;
+    const int p_min = p.causal ? off : w.len - 1, p_max = w.len - 1;
+    const KvRange range = kv_range(p_min, p_max, p.window, p.sinks);
+    const int lo_max = p.window > 0 ? p_max - p.window + 1 : 0;  // the last row's window starts here
+    int pos[2];  // position of rows n and n + 8; -1 for rows behind the last (nothing visible)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m[mt][e] = -INFINITY;
-      l[mt][e] = 0.f;
+      const int r = w.r0 + 8 * e + n;
+      pos[e] = r >= w.rows ? -1 : p.causal ? r / p.G + off : w.len - 1;
     }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[kSteps][2][4];  // [chunk of 16 d][even / odd d][C fragment]
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[mt][k][e >> 2][e & 3] = 0.f;
-  }
-
-  if (warp == 4) {
-    // ================================================================ loads
-    const int ppt = kKvTile / p.page;  // pages per tile: one per lane
-    auto first_token = [&](int t) { return (t < w.range.ns ? t : t + w.range.gap) * kKvTile + lane * p.page; };
-    auto page_of = [&](int t) -> int {  // -1: nothing to load
-      if (t >= t1 || lane >= ppt) return -1;
-      const int a = first_token(t);
-      if (!kv_needed(w.range, a, p.page)) return -1;
-      const int id = p.table[static_cast<size_t>(b) * p.width + a / p.page];
-      if (kv_page_ok(id, p.num_pages)) return id;
-      record_error(p.status, kErrBadPage, 0);
-      return -1;
-    };
-    int next = page_of(t0);
-    int done = 0;
-    for (int t = t0; t < t1; ++t, ++done) {
-      const int s = done % L::kStages;
-      const int id = next;
-      next = page_of(t + 1);
-      const size_t ph = static_cast<size_t>(id < 0 ? 0 : id) * p.Hk + hk;
-      float ks = 0.f, vs = 1.f;
-      if (id >= 0) {
-        ks = p.k_scale[ph];
-        vs = p.v_scale[ph];
-      }
-      if (!ptx::mbar_wait_warp(empty(s), ((done / L::kStages) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
-        if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteLoad);
-        break;
-      }
-      if (id >= 0) {
-        mbar_expect_tx(full(s), 2 * p.page * D);
-        const uint32_t dst = base + s * L::kStageBytes + lane * p.page * D;
-        const int row = static_cast<int>(ph) * p.page;
-        tma_load_2d(dst, &tm_k, full(s), 0, row);
-        tma_load_2d(dst + L::kTileBytes, &tm_v, full(s), 0, row);
-      }
-      if (lane < ppt) {
-        float* const cst = reinterpret_cast<float*>(gbase + L::kOffConst + s * L::kConstBytes) + 3 * lane;
-        cst[0] = ks;
-        cst[1] = log2f(vs);
-        cst[2] = 1.f / vs;
-      }
-      ptx::mbar_arrive(full(s));
-    }
-    // Nothing may land in shared memory after this: each lane sees the last fills complete.
-    for (int s = 0; s < L::kStages; ++s)
-      if (done > s) ptx::mbar_wait_drain(full(s), ((done - 1 - s) / L::kStages) & 1u, p.timeout_ns);
-  } else {
-    // ============================================================== compute
-    // q of this thread's rows n and n + 8 of each row tile, scaled to below 2^8, as
-    // A fragments: k-step kk = 4 h + wd takes d = 16 (c + 4 h) + 4 wd + {0, 1 | 2, 3}.
-    uint32_t qa[MT == 1 ? kSteps : 1][4];
-    float coef[MT][2];
-    int pos[MT][2];  // position of the row; -1 for rows behind the last (nothing visible)
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      uint32_t frag[kSteps][4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = w.r0 + 16 * mt + 8 * e + n;
-        const bool in = r < w.r1;
-        const int i = r / p.G, g = r % p.G;
-        pos[mt][e] = !in ? -1 : p.causal ? i + w.len - w.n_q : w.len - 1;
-        const __nv_bfloat16* src = p.q + (static_cast<size_t>(w.row0 + i) * p.H + hk * p.G + g) * D;
-        float x[kSteps][4];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (in) raw = *reinterpret_cast<const uint4*>(src + 16 * (c + 4 * h) + 8 * v);
-            const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[4 * h + 2 * v + (k >> 1)][2 * (k & 1)] = __uint_as_float(wd[k] << 16);
-              x[4 * h + 2 * v + (k >> 1)][2 * (k & 1) + 1] = __uint_as_float(wd[k] & 0xffff0000u);
-              amax = max(amax, max((wd[k] << 16) & 0x7fffffffu, wd[k] & 0x7fff0000u));
-            }
-          }
-        }
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // Exponent that brings the row's largest magnitude to [2^7, 2^8).
-        const int ex = min(max(static_cast<int>(amax >> 23) - 127 - 7, -119), 119);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        coef[mt][e] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * p.scale_log2;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          frag[k][e] = pack_f16x2(x[k][0] * down, x[k][1] * down);
-          frag[k][2 + e] = pack_f16x2(x[k][2] * down, x[k][3] * down);
-        }
-      }
-      if constexpr (MT == 1) {
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) qa[k][e] = frag[k][e];
-      } else if (warp == mt % 4) {
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          ptx::st_shared_v4(base + L::kOffQ + ((mt * kSteps + k) * 32 + lane) * 16, frag[k][0], frag[k][1], frag[k][2],
-                            frag[k][3]);
-      }
-    }
-    if constexpr (MT > 1) asm volatile("bar.sync 1, 128;" ::: "memory");
-
-    const int page_shift = 31 - __clz(p.page);
-    const int lo_max = p.window > 0 ? w.p_max - p.window + 1 : 0;  // the last row's window starts here
-    bool ok = true;
-    int done = 0;
+      for (int e = 0; e < 8; ++e) acc[k][e >> 2][e & 3] = 0.f;
 #pragma unroll 1
-    for (int t = t0; t < t1 && ok; ++t, ++done) {
+    for (int i = 0; i < w.steps; ++i, ++done) {
       const int s = done % L::kStages;
-      const int tok0 = (t < w.range.ns ? t : t + w.range.gap) * kKvTile + 32 * warp;
+      const int t = w.t0 + i;
+      const int tok0 = (t < w.ns ? t : t + w.gap) * kKvTile + 32 * warp;
       if (!ptx::mbar_wait_warp(full(s), (done / L::kStages) & 1u, s_abort, p.timeout_ns)) {
         if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteCompute);
-        ok = false;
-        break;
+        return;
       }
-      if (kv_needed(w.range, tok0, 32)) {
+      if (kv_needed(range, tok0, 32)) {
         const uint32_t kt = base + s * L::kStageBytes + 32 * warp * D;
         const uint32_t vt = kt + L::kTileBytes;
         const float* const cst = reinterpret_cast<const float*>(gbase + L::kOffConst + s * L::kConstBytes);
-        float sc[MT][4][4];
+        float sc[4][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sc[mt][e >> 2][e & 3] = 0.f;
+        for (int e = 0; e < 16; ++e) sc[e >> 2][e & 3] = 0.f;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
           uint4 raw[4];
@@ -355,31 +478,18 @@ __global__ void __launch_bounds__(kKvThreads, D == 128 && MT > 1 ? 1 : 2)
           for (int j = 0; j < 4; ++j) raw[j] = ld_shared_v4(kt + kv_chunk<D>(8 * j + kv_perm<D>(n), c + 4 * h));
 #pragma unroll
           for (int wd = 0; wd < 4; ++wd) {
-            uint32_t a[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              if constexpr (MT == 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a[mt][e] = qa[4 * h + wd][e];
-              } else {
-                const uint4 f = ld_shared_v4(base + L::kOffQ + ((mt * kSteps + 4 * h + wd) * 32 + lane) * 16);
-                a[mt][0] = f.x;
-                a[mt][1] = f.y;
-                a[mt][2] = f.z;
-                a[mt][3] = f.w;
-              }
-            }
+            const uint4 f = ld_shared_v4(qf + (4 * h + wd) * 512);
+            const uint32_t a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t b0, b1;
               e4m3x4_to_f16(wd == 0 ? raw[j].x : wd == 1 ? raw[j].y : wd == 2 ? raw[j].z : raw[j].w, b0, b1);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][j], a[mt], b0, b1);
+              mma_f16(sc[j], a, b0, b1);
             }
           }
         }
         // Exponents x, masked where a border runs through these 32 tokens.
-        const bool border = tok0 + 31 > w.p_min || (tok0 < lo_max && tok0 + 31 >= p.sinks);
+        const bool border = tok0 + 31 > p_min || (tok0 < lo_max && tok0 + 31 >= p.sinks);
         float inv[4];
         uint32_t vmask[4] = {~0u, ~0u, ~0u, ~0u};  // bytes of V fragments whose token no row sees
 #pragma unroll
@@ -389,69 +499,61 @@ __global__ void __launch_bounds__(kKvThreads, D == 128 && MT > 1 ? 1 : 2)
           inv[j] = pc[2];
           const int ta = tok0 + 8 * j + kv_perm<D>(2 * c), tb = tok0 + 8 * j + kv_perm<D>(2 * c + 1);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float f = coef[mt][e] * ck;
-              float x0 = fmaf(sc[mt][j][2 * e], f, lv), x1 = fmaf(sc[mt][j][2 * e + 1], f, lv);
-              if (border) {
-                const int pr = pos[mt][e], lo = p.window > 0 ? pr - p.window + 1 : 0;
-                if (ta > pr || (ta < lo && ta >= p.sinks)) x0 = -INFINITY;
-                if (tb > pr || (tb < lo && tb >= p.sinks)) x1 = -INFINITY;
-              }
-              sc[mt][j][2 * e] = x0;
-              sc[mt][j][2 * e + 1] = x1;
+          for (int e = 0; e < 2; ++e) {
+            const float f = coef[e] * ck;
+            float x0 = fmaf(sc[j][2 * e], f, lv), x1 = fmaf(sc[j][2 * e + 1], f, lv);
+            if (border) {
+              const int pr = pos[e], lo = p.window > 0 ? pr - p.window + 1 : 0;
+              if (ta > pr || (ta < lo && ta >= p.sinks)) x0 = -INFINITY;
+              if (tb > pr || (tb < lo && tb >= p.sinks)) x1 = -INFINITY;
             }
+            sc[j][2 * e] = x0;
+            sc[j][2 * e + 1] = x1;
+          }
           if (border) {
-            if (!kv_needed(w.range, ta, 1)) vmask[j] &= 0xff00ff00u;
-            if (!kv_needed(w.range, tb, 1)) vmask[j] &= 0x00ff00ffu;
+            if (!kv_needed(range, ta, 1)) vmask[j] &= 0xff00ff00u;
+            if (!kv_needed(range, tb, 1)) vmask[j] &= 0x00ff00ffu;
           }
         }
         // The reference maximum moves when a row's maximum passes it by 2^8.
         bool move = false;
-        float mx[MT][2];
+        float mx[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(sc[0][2 * e], sc[0][2 * e + 1]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) v = ptx::fmax3(v, sc[j][2 * e], sc[j][2 * e + 1]);
+          mx[e] = v;
+          move = move || v > m[e] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          float al[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = fmaxf(sc[mt][0][2 * e], sc[mt][0][2 * e + 1]);
-#pragma unroll
-            for (int j = 1; j < 4; ++j) v = ptx::fmax3(v, sc[mt][j][2 * e], sc[mt][j][2 * e + 1]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            mx[mt][e] = v;
-            move = move || v > m[mt][e] + 8.f;
+            // The four threads of a row agree on its maximum.
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+            const bool up = mx[e] > m[e] + 8.f;
+            al[e] = up ? ptx::ex2(m[e] - mx[e]) : 1.f;  // 0 from m = -inf
+            if (up) m[e] = mx[e];
+            l[e] *= al[e];
           }
-        if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float al[2];
+          for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool up = mx[mt][e] > m[mt][e] + 8.f;
-              al[e] = up ? ptx::ex2(m[mt][e] - mx[mt][e]) : 1.f;  // 0 from m = -inf
-              if (up) m[mt][e] = mx[mt][e];
-              l[mt][e] *= al[e];
-            }
+            for (int e = 0; e < 8; ++e) acc[k][e >> 2][e & 3] *= al[(e >> 1) & 1];
+        }
+        uint32_t pa[2][4];  // P as A fragments of two k-steps of 16 tokens
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k)
+        for (int e = 0; e < 2; ++e) {
+          const float neg = m[e] == -INFINITY ? 0.f : -m[e];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) acc[mt][k][e >> 2][e & 3] *= al[(e >> 1) & 1];
+          for (int j = 0; j < 4; ++j) {
+            const float e0 = ptx::ex2(sc[j][2 * e] + neg), e1 = ptx::ex2(sc[j][2 * e + 1] + neg);
+            l[e] = fmaf(e0 + e1, inv[j], l[e]);
+            pa[j >> 1][2 * (j & 1) + e] = pack_f16x2(e0, e1);
           }
         }
-        uint32_t pa[MT][2][4];  // P as A fragments of two k-steps of 16 tokens
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float neg = m[mt][e] == -INFINITY ? 0.f : -m[mt][e];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float e0 = ptx::ex2(sc[mt][j][2 * e] + neg), e1 = ptx::ex2(sc[mt][j][2 * e + 1] + neg);
-              l[mt][e] = fmaf(e0 + e1, inv[j], l[mt][e]);
-              pa[mt][j >> 1][2 * (j & 1) + e] = pack_f16x2(e0, e1);
-            }
-          }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           // Matrix lane / 8: tokens 8 (bit 0) of the 16, chunk (bit 1) of the pair.
@@ -470,95 +572,120 @@ __global__ void __launch_bounds__(kKvThreads, D == 128 && MT > 1 ? 1 : 2)
               uint32_t e0, o0, e1, o1;
               e4m3x4_to_f16(u0, e0, o0);
               e4m3x4_to_f16(u1, e1, o1);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma_f16(acc[mt][ch + q2][0], pa[mt][kk], e0, e1);
-                mma_f16(acc[mt][ch + q2][1], pa[mt][kk], o0, o1);
-              }
+              mma_f16(acc[ch + q2][0], pa[kk], e0, e1);
+              mma_f16(acc[ch + q2][1], pa[kk], o0, o1);
             }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(empty(s));
+      // The unit's last stage is kept for the warps' meeting below.
+      if (lane == 0 && i + 1 < w.steps) ptx::mbar_arrive(empty(s));
     }
-  }
+    if (lane == 0) ptx::mbar_arrive(q_empty(us));
 
-  // ------------------------------------------------- the four warps' parts joined
-  __syncthreads();
-  float* const sm_m = reinterpret_cast<float*>(gbase);
-  float* const sm_l = sm_m + 4 * RG;
-  float* const sm_o = sm_l + 4 * RG;
-  if (warp < 4) {
+    // ----------------------------------------------- the warps' parts: 2, 3 to 0, 1; 1 to 0
+    const int last = (done - 1) % L::kStages;
+    float* const area = reinterpret_cast<float*>(gbase + last * L::kStageBytes);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    }
+    auto put = [&](float* a) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 16 * mt + 8 * e + n;
-        float lt = l[mt][e] + __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
-        lt += __shfl_xor_sync(0xffffffffu, lt, 2);
-        if (c == 0) {
-          sm_m[warp * RG + r] = m[mt][e];
-          sm_l[warp * RG + r] = lt;
+        float* const dst = a + (8 * e + n) * (L::kRowStride + 2);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          *reinterpret_cast<float2*>(dst + 16 * k + 4 * c) = make_float2(acc[k][0][2 * e], acc[k][1][2 * e]);
+          *reinterpret_cast<float2*>(dst + 16 * k + 4 * c + 2) = make_float2(acc[k][0][2 * e + 1], acc[k][1][2 * e + 1]);
         }
-        float* const dst = sm_o + (warp * RG + r) * L::kRowStride + 4 * c;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          *reinterpret_cast<float4*>(dst + 16 * k) = make_float4(acc[mt][k][0][2 * e], acc[mt][k][1][2 * e],
-                                                                 acc[mt][k][0][2 * e + 1], acc[mt][k][1][2 * e + 1]);
+        if (c == 0) *reinterpret_cast<float2*>(dst + L::kRowStride) = make_float2(m[e], l[e]);
       }
-  }
-  __syncthreads();
-  const size_t all_rows = static_cast<size_t>(p.B) * p.H * p.max_q;
-  for (int idx = threadIdx.x; idx < (w.r1 - w.r0) * (D / 4); idx += kKvThreads) {
-    const int r = idx / (D / 4), d4 = idx % (D / 4);
-    const int i = (w.r0 + r) / p.G, h = hk * p.G + (w.r0 + r) % p.G;
-    float M = -INFINITY;
+    };
+    auto take = [&](const float* a) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) M = fmaxf(M, sm_m[k * RG + r]);
-    float lt = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        const float* const src = a + (8 * e + n) * (L::kRowStride + 2);
+        const float2 ml = *reinterpret_cast<const float2*>(src + L::kRowStride);
+        const float M = fmaxf(m[e], ml.x);
+        const float f0 = M == -INFINITY ? 0.f : ptx::ex2(m[e] - M), f1 = M == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
+        m[e] = M;
+        l[e] = l[e] * f0 + ml.y * f1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float f = M == -INFINITY ? 0.f : ptx::ex2(sm_m[k * RG + r] - M);
-      const float4 v = *reinterpret_cast<const float4*>(sm_o + (k * RG + r) * L::kRowStride + 4 * d4);
-      lt = fmaf(f, sm_l[k * RG + r], lt);
-      o0 = fmaf(f, v.x, o0);
-      o1 = fmaf(f, v.y, o1);
-      o2 = fmaf(f, v.z, o2);
-      o3 = fmaf(f, v.w, o3);
+        for (int k = 0; k < kSteps; ++k) {
+          const float2 x = *reinterpret_cast<const float2*>(src + 16 * k + 4 * c);
+          const float2 y = *reinterpret_cast<const float2*>(src + 16 * k + 4 * c + 2);
+          acc[k][0][2 * e] = acc[k][0][2 * e] * f0 + x.x * f1;
+          acc[k][1][2 * e] = acc[k][1][2 * e] * f0 + x.y * f1;
+          acc[k][0][2 * e + 1] = acc[k][0][2 * e + 1] * f0 + y.x * f1;
+          acc[k][1][2 * e + 1] = acc[k][1][2 * e + 1] * f0 + y.y * f1;
+        }
+      }
+    };
+    constexpr int kArea = kKvRows * (L::kRowStride + 2);
+    if (!meet()) return;  // all four have read the stage
+    if (warp >= 2) put(area + (warp - 2) * kArea);
+    if (!meet()) return;
+    if (warp < 2) take(area + warp * kArea);
+    if (warp == 1) put(area + kArea);
+    if (!meet()) return;
+    if (warp == 0) {
+      take(area + kArea);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = w.r0 + 8 * e + n;
+        if (r >= w.rows) continue;
+        const float il = l[e] > 0.f ? 1.f / l[e] : l[e];  // NaN stays
+        const float lse2 = l[e] > 0.f ? m[e] + log2f(l[e]) : l[e] == 0.f ? -INFINITY : l[e];
+        if (w.place >= 0) {
+          const size_t row = static_cast<size_t>(w.place) * kKvRows + 8 * e + n;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            *reinterpret_cast<float4*>(p.part_o + row * D + 16 * k + 4 * c) =
+                make_float4(acc[k][0][2 * e] * il, acc[k][1][2 * e] * il, acc[k][0][2 * e + 1] * il,
+                            acc[k][1][2 * e + 1] * il);
+          if (c == 0) p.part_lse[row] = lse2;
+        } else {
+          const int i = r / p.G, h = w.hk * p.G + r % p.G;
+          __nv_bfloat16* const dst = p.o + (static_cast<size_t>(w.row0 + i) * p.H + h) * D + 4 * c;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            *reinterpret_cast<uint2*>(dst + 16 * k) =
+                make_uint2(ptx::pack_bf16x2(acc[k][0][2 * e] * il, acc[k][1][2 * e] * il),
+                           ptx::pack_bf16x2(acc[k][0][2 * e + 1] * il, acc[k][1][2 * e + 1] * il));
+          if (c == 0) p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.max_q + i] = lse2 * 0.69314718055994530942f;
+        }
+      }
     }
-    const float il = lt > 0.f ? 1.f / lt : 0.f;
-    const float lse2 = lt > 0.f ? M + log2f(lt) : -INFINITY;
-    const size_t row = (static_cast<size_t>(b) * p.H + h) * p.max_q + i;
-    if (p.splits > 1) {
-      const size_t at = static_cast<size_t>(split) * all_rows + row;
-      *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * d4) = make_float4(o0 * il, o1 * il, o2 * il, o3 * il);
-      if (d4 == 0) p.ws_lse[at] = lse2;
-    } else {
-      uint2 pk = make_uint2(ptx::pack_bf16x2(o0 * il, o1 * il), ptx::pack_bf16x2(o2 * il, o3 * il));
-      if (!(lt > 0.f) && M == -INFINITY) pk = make_uint2(0u, 0u);
-      *reinterpret_cast<uint2*>(p.o + (static_cast<size_t>(w.row0 + i) * p.H + h) * D + 4 * d4) = pk;
-      if (d4 == 0) p.lse[row] = lse2 * 0.69314718055994530942f;
-    }
+    // The stage goes back to TMA: order the writes above before its copies.
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(empty(last));
   }
 }
 
-// The splits of each row joined: o = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse2_s - max).
-// One warp per row; bound by reading the fp32 parts (a few per cent of the codes).
-template <int D, int RG>
+// The parts of the unit that ends in CTA blockIdx.x's range and was begun before
+// it: o = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse2_s - max).  One block per row;
+// each warp adds every fourth part.  Bound by reading the parts, a few per cent of
+// the codes; a single sequence and head has one part per CTA.
+template <int D>
 __global__ void __launch_bounds__(128) fa_kv_join_kernel(const KvAttnParams p) {
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const long long all_rows = static_cast<long long>(p.B) * p.H * p.max_q;
-  if (row >= all_rows) return;
-  const int i = static_cast<int>(row % p.max_q);
-  const int h = static_cast<int>((row / p.max_q) % p.H);
-  const int b = static_cast<int>(row / p.max_q / p.H);
-  const KvWork w = kv_work<RG>(p, b, (i * p.G + h % p.G) / RG);
-  if (i >= w.n_q) return;
-  const int parts = (w.range.steps + p.split_steps - 1) / p.split_steps;
+  const int4 cut = p.cut[blockIdx.x];
+  if (cut.x < 0) return;
+  const int r = cut.z + blockIdx.y;
+  const int row0 = p.cu ? p.cu[cut.x] : cut.x * p.max_q;
+  const int n_q = p.cu ? p.cu[cut.x + 1] - row0 : p.max_q;
+  if (r >= n_q * p.G) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = static_cast<int>(blockIdx.x) - cut.w + 1;
+  // Part s lies with CTA cut.w + s: the first is that CTA's tail, the others are heads.
+  auto at = [&](int s) -> size_t {
+    return (2 * static_cast<size_t>(cut.w + s) + (s == 0 ? 1 : 0)) * kKvRows + blockIdx.y;
+  };
   float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.ws_lse[s * all_rows + row]);
+  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_lse[at(s)]);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
   constexpr int kPer = D / 32;
@@ -567,20 +694,32 @@ __global__ void __launch_bounds__(128) fa_kv_join_kernel(const KvAttnParams p) {
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   if (M > -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-      const float f = ptx::ex2(p.ws_lse[s * all_rows + row] - M);
-      const float* src = p.ws_o + (s * all_rows + row) * D + lane * kPer;
+    for (int s = warp; s < parts; s += 4) {
+      const float f = ptx::ex2(p.part_lse[at(s)] - M);
+      const float* src = p.part_o + at(s) * D + lane * kPer;
       l += f;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] = fmaf(f, src[e], acc[e]);
     }
   }
-  const float il = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* const dst = p.o + (static_cast<size_t>(w.row0 + i) * p.H + h) * D + lane * kPer;
+  __shared__ float s_acc[4][D], s_l[4];
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack_bf16x2(acc[e] * il, acc[e + 1] * il);
-  if (lane == 0) p.lse[row] = l > 0.f ? (M + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+  for (int e = 0; e < kPer; ++e) s_acc[warp][lane * kPer + e] = acc[e];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const float il = l > 0.f ? 1.f / l : 0.f;
+  const int i = r / p.G, h = cut.y * p.G + r % p.G;
+  if (threadIdx.x < D / 2) {
+    const int e = 2 * threadIdx.x;
+    const float a = (s_acc[0][e] + s_acc[1][e]) + (s_acc[2][e] + s_acc[3][e]);
+    const float c = (s_acc[0][e + 1] + s_acc[1][e + 1]) + (s_acc[2][e + 1] + s_acc[3][e + 1]);
+    *reinterpret_cast<uint32_t*>(p.o + (static_cast<size_t>(row0 + i) * p.H + h) * D + e) =
+        ptx::pack_bf16x2(a * il, c * il);
+  }
+  if (threadIdx.x == 0)
+    p.lse[(static_cast<size_t>(cut.x) * p.H + h) * p.max_q + i] =
+        l > 0.f ? (M + log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace fa
