@@ -35,7 +35,7 @@ KvPlan kv_plan(int B, int max_q, int max_k, int H, int Hk, int d, int causal, in
   z.few = rows <= kFewRows;
   if (!z.few) {
     z.k_pad = (max_k + kKvTile - 1) / kKvTile * kKvTile;
-    z.ws_bytes = 2 * static_cast<size_t>(B) * z.k_pad * Hk * d * 2;
+    z.ws_bytes = 2 * static_cast<size_t>(B) * z.k_pad * Hk * d * 2 + window_parts_bytes(num_sms, d);
     return z;
   }
   long long steps = (static_cast<long long>(max_k) + kKvTile - 1) / kKvTile;
@@ -284,6 +284,7 @@ int fa_fwd_kvcache(const void* q, const void* k8, const void* v8, const float* k
   p.scale = scale;
   p.timeout_ns = dev.timeout_ns;
   p.status = dev.status;
+  fa::window_parts(p, dq.v + static_cast<size_t>(B) * z.k_pad * Hk * d, dev.num_sms);
   a.num_sms = dev.num_sms;
   a.stream = st;
   return fa::launch_window(a, q, z.k_pad > 0 ? static_cast<const void*>(dq.k) : q,

@@ -37,10 +37,26 @@
 
 namespace fa {
 
-// Key tiles [0, nsk) hold sinks; a query tile whose window starts in key tile
-// `lo` and whose diagonal ends in `hi` sees key tile kt under this rule.
-__host__ __device__ __forceinline__ bool win_sees(int kt, int lo, int hi, int nsk) {
-  return kt <= hi && (kt < nsk || kt >= lo);
+// The steps of a unit that a query tile takes part in: j < s (tiles with sinks) and
+// a <= j < e (its window).
+struct WinSteps {
+  int s, a, e;
+};
+// Key tiles [0, nsk) hold sinks; the query tile's window starts in key tile `lo`
+// and its diagonal ends in `hi`; step j of the unit is key tile j for j < ns, else
+// j + gap (gap > 0 only behind all sink tiles).
+__host__ __device__ __forceinline__ WinSteps win_steps(int lo, int hi, int nsk, int ns, int gap) {
+  WinSteps w;
+  w.s = gap > 0 ? ns : (nsk < hi + 1 ? nsk : hi + 1);
+  w.a = lo - gap;
+  w.e = hi - gap + 1;
+  return w;
+}
+__host__ __device__ __forceinline__ bool win_sees(const WinSteps& w, int j) { return j < w.s || (j >= w.a && j < w.e); }
+// The last such step in [j0, j1), -1 if there is none.
+__host__ __device__ __forceinline__ int win_last(const WinSteps& w, int j0, int j1) {
+  const int x = (j1 < w.e ? j1 : w.e) - 1, y = (j1 < w.s ? j1 : w.s) - 1;
+  return x >= w.a && x >= j0 ? x : y >= j0 ? y : -1;
 }
 
 // The low n bits set (none for n <= 0, all for n >= 32).
@@ -51,24 +67,19 @@ struct WinUnit {
   int q_start, q_end, k_start, k_end;
   int q_row0;
   int off;        // position of query i is i + off
-  int nsk;        // key tiles that hold sinks
   int ns, gap;    // steps [0, ns) are key tiles 0..ns-1; step j >= ns is key tile j + gap
   int nsteps;
+  int j0, j1;     // the steps of this item: all, or (KPAD) a range of them
+  int place;      // -1: o and lse are written; else the item's place for partial results
   int lse_base;
   bool run, nokeys;
-  bool active[kQT];  // tile t has rows and sees keys
-  bool zero[kQT];    // tile t has rows and sees none
-  int lo[kQT], hi[kQT];  // first key tile of the window, last key tile (diagonal)
+  bool rows[kQT];    // tile t has rows
+  bool active[kQT];  // tile t has rows and sees keys of these steps
+  WinSteps st[kQT];  // empty where tile t is not active
+  int last[kQT];     // the last step that tile t takes part in
   RowWindow qwin[kQT];
   __device__ __forceinline__ int kt(int j) const { return j < ns ? j : j + gap; }
-  __device__ __forceinline__ bool sees(int t, int j) const {
-    return (t == 0 ? active[0] : active[1]) && win_sees(kt(j), t == 0 ? lo[0] : lo[1], t == 0 ? hi[0] : hi[1], nsk);
-  }
-  // Step after which query tile t is complete (its diagonal tile).
-  __device__ __forceinline__ int last(int t) const {
-    const int e = t == 0 ? hi[0] : hi[1];
-    return e < ns ? e : e - gap;
-  }
+  __device__ __forceinline__ bool sees(int t, int j) const { return win_sees(t == 0 ? st[0] : st[1], j); }
 };
 
 struct WinParams {
@@ -85,9 +96,28 @@ struct WinParams {
   __nv_bfloat16* o;
   float scale, scale_log2;
   float rescale_threshold;
+  // KPAD: a unit cut by the borders of CTA c's range of steps lies at place 2c (begun
+  // by an earlier CTA) or 2c + 1 (begun by c, ended later); cut[c] names the unit
+  // that ends in c and was begun by an earlier CTA.
+  int2* cut;                   // [ctas]: unit (-1: none), CTA that began it
+  float* part_o;               // [2 ctas, 256, d], normalised
+  float* part_lse;             // [2 ctas, 256]
   unsigned long long timeout_ns;
   int* status;
 };
+
+// Restricts a unit to the steps [j0, j1).
+__device__ __forceinline__ void win_restrict(WinUnit& w, int j0, int j1, int place) {
+  w.j0 = j0;
+  w.j1 = j1;
+  w.place = place;
+#pragma unroll
+  for (int t = 0; t < kQT; ++t) {
+    w.last[t] = win_last(w.st[t], j0, j1);
+    w.active[t] = w.last[t] >= 0;
+  }
+  w.run = w.active[0] || w.active[1];
+}
 
 template <int BC, bool VARLEN, bool KPAD>
 __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
@@ -124,46 +154,74 @@ __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
   w.off = (w.k_end - w.k_start) - (w.q_end - w.q_start);
   w.lse_base = (w.b * p.H + w.h) * p.Nq;
   const bool has_rows = !bad && w.q_row0 < w.q_end;
-  const int sinks = min(p.sinks, len_k);
-  w.nsk = (sinks + BC - 1) / BC;
-  int first = 0x7fffffff, end = -1;
+  const int nsk = (min(p.sinks, len_k) + BC - 1) / BC;  // key tiles that hold sinks
+  int first = 0x7fffffff, end = -1, lo[kQT], hi[kQT];
 #pragma unroll
   for (int t = 0; t < kQT; ++t) {
     const int r0 = w.q_row0 + t * kBR;
     w.qwin[t] = make_window<VARLEN>(w.q_start, w.q_end, r0, kBR);
-    const bool rows = has_rows && r0 < w.q_end;
+    w.rows[t] = has_rows && r0 < w.q_end;
     // Positions of the tile's first and last row of its own.
     const int p0 = p.full ? len_k - 1 : w.qwin[t].load_row - w.q_start + w.qwin[t].lo + w.off;
     const int p1 = p.full ? len_k - 1 : w.qwin[t].load_row - w.q_start + w.qwin[t].hi - 1 + w.off;
-    w.active[t] = rows && len_k > 0 && p1 >= 0;
-    w.zero[t] = rows && len_k > 0 && p1 < 0;
-    w.lo[t] = max(0, p0 - p.window + 1) / BC;  // window <= the longest sequence
-    w.hi[t] = p1 < 0 ? -1 : p1 / BC;           // p1 <= len_k - 1
+    w.active[t] = w.rows[t] && len_k > 0 && p1 >= 0;
+    lo[t] = max(0, p0 - p.window + 1) / BC;  // window <= the longest sequence
+    hi[t] = p1 < 0 ? -1 : p1 / BC;           // p1 <= len_k - 1
     if (w.active[t]) {
-      first = min(first, w.lo[t]);
-      end = max(end, w.hi[t]);
+      first = min(first, lo[t]);
+      end = max(end, hi[t]);
     }
   }
   w.run = w.active[0] || w.active[1];
   w.nokeys = has_rows && len_k == 0;
-  w.ns = w.run ? min(w.nsk, first) : 0;
+  w.ns = w.run ? min(nsk, first) : 0;
   w.gap = w.run ? first - w.ns : 0;
   w.nsteps = w.run ? w.ns + end - first + 1 : 0;
+#pragma unroll
+  for (int t = 0; t < kQT; ++t) w.st[t] = w.active[t] ? win_steps(lo[t], hi[t], nsk, w.ns, w.gap) : WinSteps{0, 0, 0};
+  win_restrict(w, 0, w.nsteps, -1);
   if (bad && mb == 0 && w.h == 0) {
     if ((threadIdx.x & 31) == 0 && threadIdx.x < 32) record_error(p.status, kErrBadSeqlens, 0);
   }
   return w;
 }
 
-// Dense problems walk units blockIdx.x + k * gridDim.x on a grid of one CTA per
-// SM; packed batches launch one CTA per unit and take over units not yet
-// started (the item ring of fa_fwd_kernel.cuh).
-#define FA_WIN_NEXT(prev)                                                                             \
-  (VARLEN ? item_next(bar(L::kBarItemFull), bar(L::kBarItemEmpty), s_items, s_abort, tmo, p.status,    \
-                      item_n_, warp != 12)                                                           \
-          : ((prev) < 0 ? static_cast<int>(blockIdx.x) : (prev) + static_cast<int>(gridDim.x)))
-#define FA_WIN_FOR_EACH_UNIT(u) \
-  for (int u = FA_WIN_NEXT(-1); u >= 0 && u < p.num_units && ok; u = FA_WIN_NEXT(u))
+// Items reach the roles in one of three ways.
+//   Dense: units blockIdx.x + k * gridDim.x on a grid of one CTA per SM.
+//   Packed: one CTA per unit is launched, a running CTA takes over units not yet
+//     started (cluster launch control), through the ring of fa_fwd_kernel.cuh.
+//   KPAD (few queries, many keys): the steps of all units, laid end to end, are cut
+//     into one range per SM; the load thread hands units, and the parts of units
+//     cut by the range's borders, through the ring; fa_win_join_kernel joins the
+//     parts.  Three prompts of at most 1024 queries over 8192 keys, 16 heads: 92 us
+//     of whole units left most SMs idle behind the longest (195 us).
+struct WinItem {
+  int u, j0, j1, place;  // u < 0: no more
+};
+
+// Shared memory behind the tiles: the ring's items, and the scan of the lengths.
+template <int D, int STAGES>
+struct WinSmem {
+  using L = SmemLayout<D, 128, STAGES>;
+  static constexpr int kOffItems = (L::kBytes + 15) / 16 * 16;
+  static constexpr int kOffScan = kOffItems + kItemSlots * 16;
+  static constexpr int kBytes = kOffScan + (kThreads / 32 + 2) * 8;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 232448, "shared memory budget exceeded");
+};
+
+// KPAD: steps of unit (b, query block mb) of any head, at least one where it has rows.
+template <bool VARLEN>
+__device__ __forceinline__ int win_flat(const WinParams& p, int b, int mb) {
+  const WinUnit w = win_decode<128, VARLEN, true>(p, b * p.H * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - mb : mb));
+  return w.rows[0] ? max(w.nsteps, 1) : 0;
+}
+
+#define FA_WIN_FOR_EACH_ITEM(it) \
+  for (WinItem it = next_item(-1); it.u >= 0 && it.u < p.num_units && ok; it = next_item(it.u))
+#define FA_WIN_UNIT(it)                                       \
+  WinUnit w = win_decode<BC, VARLEN, KPAD>(p, (it).u);        \
+  if constexpr (KPAD) win_restrict(w, (it).j0, (it).j1, (it).place)
 
 template <int D, int STAGES, bool VARLEN, bool KPAD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -189,9 +247,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* const s_invl = reinterpret_cast<float*>(gbase + L::kOffInvL);
   volatile uint32_t* const s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + L::kOffTmem);
   volatile int* const s_abort = reinterpret_cast<volatile int*>(gbase + L::kOffAbort);
-  volatile int* const s_items = reinterpret_cast<volatile int*>(gbase + L::kOffItems);
+  volatile WinItem* const s_items = reinterpret_cast<volatile WinItem*>(gbase + WinSmem<D, STAGES>::kOffItems);
   const uint64_t tmo = p.timeout_ns;
   uint32_t item_n_ = 0;
+  constexpr bool kRing = VARLEN || KPAD;
+  auto next_item = [&](int prev) -> WinItem {
+    if constexpr (!kRing) {
+      return WinItem{prev < 0 ? static_cast<int>(blockIdx.x) : prev + static_cast<int>(gridDim.x), 0, 0, -1};
+    } else {
+      const bool whole = warp != 12;  // the MMA thread reads alone, the other roles warp-wide
+      const uint32_t slot = item_n_ % kItemSlots, parity = (item_n_ / kItemSlots) & 1u;
+      const bool got = whole ? ptx::mbar_wait_warp(bar(L::kBarItemFull) + 8u * slot, parity, s_abort, tmo)
+                             : ptx::mbar_wait(bar(L::kBarItemFull) + 8u * slot, parity, s_abort, tmo);
+      if (!got) {
+        if (!whole || lane == 0) record_error(p.status, kErrTimeout, kSiteItem);
+        return WinItem{-1, 0, 0, -1};
+      }
+      const WinItem it{s_items[slot].u, s_items[slot].j0, s_items[slot].j1, s_items[slot].place};
+      if (whole) __syncwarp();
+      if (!whole || lane == 0) ptx::mbar_arrive(bar(L::kBarItemEmpty) + 8u * slot);
+      ++item_n_;
+      return it;
+    }
+  };
 
   // ------------------------------------------------------------------ setup
   if (warp == 13 && lane == 0) {
@@ -227,6 +305,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(base + L::kOffTmem, kTmemCols);
     ptx::tmem_relinquish();
   }
+  // KPAD: this CTA's range [begin, end) of the steps of all units (sequence by
+  // sequence, query blocks in order, heads innermost), from a scan of the lengths.
+  long long begin = 0, end = 0, span = 1;
+  long long* const s_scan = reinterpret_cast<long long*>(gbase + WinSmem<D, STAGES>::kOffScan);
+  if constexpr (KPAD) {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    auto flat = [&](int b) -> long long {
+      long long sum = 0;
+      for (int mb = 0; mb < p.num_mblocks; ++mb) sum += win_flat<VARLEN>(p, b, mb);
+      return sum * p.H;
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += flat(b);
+    long long pre = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, pre, k);
+      if (lane >= k) pre += v;
+    }
+    if (lane == 31) s_scan[warp] = pre;
+    __syncthreads();
+    long long total = 0;
+    for (int k = 0; k < kThreads / 32; ++k) {
+      if (k < warp) pre += s_scan[k];
+      total += s_scan[k];
+    }
+    pre -= mine;
+    span = max((total + gridDim.x - 1) / gridDim.x, 1LL);
+    begin = blockIdx.x * span;
+    end = min(total, begin + span);
+    if (begin < end && begin >= pre && begin < pre + mine) {
+      long long at = pre;
+      int b = b0;
+      for (; b < b1; ++b) {
+        const long long f = flat(b);
+        if (begin < at + f) break;
+        at += f;
+      }
+      s_scan[kThreads / 32] = b;
+      s_scan[kThreads / 32 + 1] = at;
+    }
+    if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int2(-1, 0);
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -240,13 +362,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t n_pub = 0, n_clc = 0;
       bool clc_pending = false;
-      auto publish = [&](int item) -> bool {
+      auto publish = [&](const WinItem& item) -> bool {
         const uint32_t slot = n_pub % kItemSlots;
         if (!ptx::mbar_wait(bar(L::kBarItemEmpty + slot), ((n_pub / kItemSlots) & 1u) ^ 1u, s_abort, tmo)) {
           record_error(p.status, kErrTimeout, kSiteItem);
           return false;
         }
-        s_items[slot] = item;
+        s_items[slot].u = item.u;
+        s_items[slot].j0 = item.j0;
+        s_items[slot].j1 = item.j1;
+        s_items[slot].place = item.place;
         ptx::mbar_arrive(bar(L::kBarItemFull + slot));
         ++n_pub;
         return true;
@@ -257,14 +382,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::clc_try_cancel(base + L::kOffClc, bar(L::kBarClc));
         clc_pending = true;
       };
-      int cur = blockIdx.x;
-      if constexpr (VARLEN) {
-        ok = publish(cur);
+      // KPAD: where the range stands: sequence, its first step, query block, its first step.
+      int kb = 0, kmb = 0, kw = 0;
+      long long kat = 0, pos = begin;
+      if constexpr (KPAD) {
+        if (begin < end) {
+          kb = static_cast<int>(s_scan[kThreads / 32]);
+          kat = s_scan[kThreads / 32 + 1];
+          kw = win_flat<VARLEN>(p, kb, 0);
+        }
+      }
+      auto range_item = [&]() -> WinItem {
+        if (pos >= end) return WinItem{-1, 0, 0, -1};
+        while (pos >= kat + static_cast<long long>(kw) * p.H) {
+          kat += static_cast<long long>(kw) * p.H;
+          if (++kmb == p.num_mblocks) {
+            kmb = 0;
+            ++kb;
+          }
+          kw = win_flat<VARLEN>(p, kb, kmb);
+        }
+        const int h = static_cast<int>((pos - kat) / kw), j0 = static_cast<int>((pos - kat) % kw);
+        const int j1 = static_cast<int>(min(static_cast<long long>(kw), j0 + (end - pos)));
+        const int u = (kb * p.H + h) * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - kmb : kmb);
+        const int place = j0 > 0 ? 2 * static_cast<int>(blockIdx.x) : j1 < kw ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+        if (j0 > 0 && j1 == kw) p.cut[blockIdx.x] = make_int2(u, static_cast<int>((pos - j0) / span));
+        pos += j1 - j0;
+        return WinItem{u, j0, j1, place};
+      };
+      WinItem cur{static_cast<int>(blockIdx.x), 0, 0, -1};
+      if constexpr (KPAD) cur = range_item();
+      if constexpr (kRing) ok = publish(cur);
+      if constexpr (VARLEN && !KPAD) {
         if (ok) request();
       }
 #pragma unroll 1
-      while (ok && cur >= 0 && cur < p.num_units) {
-        const WinUnit w = win_decode<BC, VARLEN, KPAD>(p, cur);
+      while (ok && cur.u >= 0 && cur.u < p.num_units) {
+        FA_WIN_UNIT(cur);
         if (w.run) {
           if (!ptx::mbar_wait(bar(L::kBarQEmpty), (qcount & 1u) ^ 1u, s_abort, tmo)) {
             record_error(p.status, kErrTimeout, kSiteLoadQ);
@@ -297,35 +451,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           };
 #pragma unroll 1
-          for (int j = 0; j <= w.nsteps; ++j) {
+          for (int j = w.j0; j <= w.j1; ++j) {
             const uint32_t slot = g % STAGES;
             if (!ptx::mbar_wait(bar(L::kBarKVEmpty + slot), ((g / STAGES) & 1u) ^ 1u, s_abort, tmo)) {
               record_error(p.status, kErrTimeout, kSiteLoadKV);
               ok = false;
               break;
             }
-            const uint32_t bytes = (j < w.nsteps ? L::kKVTileBytes : 0) + (j >= 1 ? L::kKVTileBytes : 0);
+            const uint32_t bytes = (j < w.j1 ? L::kKVTileBytes : 0) + (j > w.j0 ? L::kKVTileBytes : 0);
             const uint32_t full = bar(L::kBarKVFull + slot);
             ptx::mbar_arrive_expect_tx(full, bytes);
             ++g;
             const uint32_t sbase = base + L::kOffKV + slot * L::kSlotBytes;
-            if (j < w.nsteps) load_tile(sbase, &tm_k, full, w.kt(j));
-            if (j >= 1) load_tile(sbase + L::kKVTileBytes, &tm_v, full, w.kt(j - 1));
+            if (j < w.j1) load_tile(sbase, &tm_k, full, w.kt(j));
+            if (j > w.j0) load_tile(sbase + L::kKVTileBytes, &tm_v, full, w.kt(j - 1));
           }
           if (!ok) break;
         }
-        if constexpr (VARLEN) {
+        if constexpr (KPAD) {
+          cur = range_item();
+          if (!publish(cur)) break;
+        } else if constexpr (VARLEN) {
           if (!ptx::mbar_wait(bar(L::kBarClc), n_clc & 1u, s_abort, tmo)) {
             record_error(p.status, kErrTimeout, kSiteItem);
             break;
           }
           ++n_clc;
           clc_pending = false;
-          cur = ptx::clc_cancelled_x(base + L::kOffClc);
+          cur.u = ptx::clc_cancelled_x(base + L::kOffClc);
           if (!publish(cur)) break;
-          if (cur >= 0) request();
+          if (cur.u >= 0) request();
         } else {
-          cur += gridDim.x;
+          cur.u += gridDim.x;
         }
       }
       // Nothing may land in shared memory after the CTA is gone.
@@ -352,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
       };
 #pragma unroll 1
-      FA_WIN_FOR_EACH_UNIT(u) {
-        const WinUnit w = win_decode<BC, VARLEN, KPAD>(p, u);
+      FA_WIN_FOR_EACH_ITEM(it) {
+        FA_WIN_UNIT(it);
         if (!w.run) continue;
         if (!wait(bar(L::kBarQFull), qcount & 1u, kSiteMmaQ)) break;
         ++qcount;
@@ -361,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool begun[kQT] = {false, false};  // O_t holds a partial sum of this unit
         bool held[kQT] = {false, false};   // P_t of the previous step waits for its product
 #pragma unroll 1
-        for (int j = 0; j <= w.nsteps && ok; ++j) {
+        for (int j = w.j0; j <= w.j1 && ok; ++j) {
           const uint32_t slot = g % STAGES;
           if (!wait(bar(L::kBarKVFull + slot), (g / STAGES) & 1u, kSiteMmaK)) break;
           ptx::tc_fence_after();
@@ -384,9 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mma_ts(tO, tP + kk * 8, vdesc + static_cast<uint64_t>(kk * 128), idesc_pv,
                             (begun[t] || kk > 0) ? 1u : 0u);
               begun[t] = true;
-              if (j - 1 == w.last(t)) ptx::mma_commit(bar(L::kBarOFinal + t));
+              if (j - 1 == w.last[t]) ptx::mma_commit(bar(L::kBarOFinal + t));
             }
-            held[t] = j < w.nsteps && w.sees(t, j);
+            held[t] = j < w.j1 && w.sees(t, j);
             if (held[t]) {
               // S_t = Q_t K(j)^T
               const uint64_t qdesc = ptx::sw128_desc(base + L::kOffQ + t * L::kQTileBytes, 16, 1024);
@@ -402,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!ok) break;
-          if (j == w.nsteps - 1) ptx::mma_commit(bar(L::kBarQEmpty));
+          if (j == w.j1 - 1) ptx::mma_commit(bar(L::kBarQEmpty));
           ptx::mma_commit(bar(L::kBarKVEmpty + slot));
           ++g;
         }
@@ -427,10 +584,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t units = 0;   // units of this tile finished
     bool ok = true;
 #pragma unroll 1
-    FA_WIN_FOR_EACH_UNIT(u) {
-      const WinUnit w = win_decode<BC, VARLEN, KPAD>(p, u);
-      if (!(t == 0 ? w.active[0] : w.active[1])) continue;
+    FA_WIN_FOR_EACH_ITEM(it) {
+      FA_WIN_UNIT(it);
       const RowWindow qw = t == 0 ? w.qwin[0] : w.qwin[1];
+      // Place of this row's partial results (row of the unit).
+      const size_t part = KPAD && w.place >= 0
+                              ? static_cast<size_t>(w.place) * (kBR * kQT) + (qw.load_row + row - w.q_row0)
+                              : 0;
+      if (!(t == 0 ? w.active[0] : w.active[1])) {
+        // No key of these steps in sight: a part of weight zero.
+        if (KPAD && w.place >= 0 && (t == 0 ? w.rows[0] : w.rows[1]) && row >= qw.lo && row < qw.hi)
+          p.part_lse[part] = -INFINITY;
+        continue;
+      }
       // Positions of this row and of the tile's first and last row of its own.
       const int len_k = w.k_end - w.k_start;
       const int pos = p.full ? len_k - 1 : qw.load_row - w.q_start + row + w.off;
@@ -440,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = 0.f;
       int taken = 0;  // steps of this unit taken part in
 #pragma unroll 1
-      for (int j = 0; j < w.nsteps; ++j) {
+      for (int j = w.j0; j < w.j1; ++j) {
         if (!w.sees(t, j)) continue;
         if (!ptx::mbar_wait_warp(bar(L::kBarSFull + t), sc & 1u, s_abort, tmo)) {
           record_error(p.status, kErrTimeout, kSiteSoftS);
@@ -588,9 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool has = l > 0.f;
       s_invl[t * kBR + row] = has ? 1.f / l : 0.f;
-      if (row >= qw.lo && row < qw.hi)
-        p.lse[w.lse_base + (qw.load_row - w.q_start + row)] =
-            has ? m_ref * p.scale + log2f(l) * 0.69314718055994530942f : -INFINITY;
+      if (row >= qw.lo && row < qw.hi) {
+        float* const dst = KPAD && w.place >= 0 ? p.part_lse + part : p.lse + w.lse_base + (qw.load_row - w.q_start + row);
+        *dst = has ? m_ref * p.scale + log2f(l) * 0.69314718055994530942f : -INFINITY;
+      }
       ptx::mbar_arrive(bar(L::kBarLReady + t));
       ++units;
     }
@@ -613,8 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = threadIdx.x - 256; r < rows; r += 128) p.lse[w.lse_base + (row0 - w.q_start) + r] = -INFINITY;
     };
 #pragma unroll 1
-    FA_WIN_FOR_EACH_UNIT(u) {
-      const WinUnit w = win_decode<BC, VARLEN, KPAD>(p, u);
+    FA_WIN_FOR_EACH_ITEM(it) {
+      FA_WIN_UNIT(it);
       if (w.nokeys) {
         zero_rows(w, w.q_row0, min(kBR * kQT, w.q_end - w.q_row0));
         continue;
@@ -622,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int t = 0; t < kQT; ++t) {
         const RowWindow qw = w.qwin[t];
-        if (w.zero[t]) zero_rows(w, qw.load_row + qw.lo, qw.hi - qw.lo);
+        if (w.rows[t] && !w.active[t] && !(KPAD && w.place >= 0)) zero_rows(w, qw.load_row + qw.lo, qw.hi - qw.lo);
         if (!w.active[t]) continue;
         if (!ptx::mbar_wait_warp(bar(L::kBarLReady + t), uc[t] & 1u, s_abort, tmo) ||
             !ptx::mbar_wait_warp(bar(L::kBarOFinal + t), uc[t] & 1u, s_abort, tmo)) {
@@ -635,10 +802,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv_l = s_invl[t * kBR + row];
         const uint32_t tO = tmem + lane_off + static_cast<uint32_t>(2 * BC + t * D);
         const bool warp_full = (wq << 5) >= qw.lo && (wq << 5) + 32 <= qw.hi;
-        const bool use_tma = !VARLEN || warp_full;  // dense: rows past Nq are clipped by the map
+        const bool parted = KPAD && w.place >= 0;
+        const bool use_tma = !parted && (!VARLEN || warp_full);  // dense: rows past Nq are clipped by the map
         const bool row_ok = row >= qw.lo && row < qw.hi;
         __nv_bfloat16* const grow =
             row_ok ? p.o + (static_cast<size_t>(qw.load_row + row) * p.H + w.h) * D : p.o;
+        float* const prow =
+            parted && row_ok
+                ? p.part_o + (static_cast<size_t>(w.place) * (kBR * kQT) + (qw.load_row + row - w.q_row0)) * D
+                : nullptr;
         if (use_tma && pending) {
           if (lane == 0) ptx::bulk_wait_group_read_0();
           __syncwarp();
@@ -649,6 +821,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[32];
           ptx::tmem_ld32(tO + c * 32, r);
           ptx::tmem_wait_ld();
+          if (parted) {
+            if (row_ok) {
+#pragma unroll
+              for (int q4 = 0; q4 < 8; ++q4)
+                ptx::st_global_v4(prow + c * 32 + q4 * 4, __float_as_uint(__uint_as_float(r[4 * q4]) * inv_l),
+                                  __float_as_uint(__uint_as_float(r[4 * q4 + 1]) * inv_l),
+                                  __float_as_uint(__uint_as_float(r[4 * q4 + 2]) * inv_l),
+                                  __float_as_uint(__uint_as_float(r[4 * q4 + 3]) * inv_l));
+            }
+            continue;
+          }
           uint32_t wv[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -697,6 +880,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// The parts of the unit that ends in CTA blockIdx.x's range and was begun before
+// it ("GPU 内核与 FlashAttention" §11.2): o = sum_s w_s O_s / sum_s w_s with w_s =
+// e^(LSE_s - max).  One warp per row; bound by reading the parts.
+template <int D, bool VARLEN>
+__global__ void __launch_bounds__(256) fa_win_join_kernel(const WinParams p) {
+  const int2 cut = p.cut[blockIdx.x];
+  if (cut.x < 0) return;
+  const WinUnit w = win_decode<128, VARLEN, true>(p, cut.x);
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (w.q_row0 + r >= w.q_end) return;
+  const int parts = static_cast<int>(blockIdx.x) - cut.y + 1;
+  auto at = [&](int s) -> size_t { return (2 * static_cast<size_t>(cut.y + s) + (s == 0 ? 1 : 0)) * (kBR * kQT) + r; };
+  float M = -INFINITY;
+  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_lse[at(s)]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+  constexpr int kPer = D / 32;
+  float acc[kPer], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float ls = p.part_lse[at(s)];
+    if (ls == -INFINITY) continue;  // a part without keys holds no values
+    const float f = ptx::ex2((ls - M) * 1.44269504088896340736f);
+    const float* src = p.part_o + at(s) * D + lane * kPer;
+    l += f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+  }
+  const float il = l > 0.f ? 1.f / l : l;
+  const size_t row = VARLEN ? static_cast<size_t>(w.q_row0 + r) : static_cast<size_t>(w.b) * p.Nq + w.q_row0 + r;
+  __nv_bfloat16* const dst = p.o + (row * p.H + w.h) * D + lane * kPer;
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack_bf16x2(acc[e] * il, acc[e + 1] * il);
+  if (lane == 0) p.lse[w.lse_base + (w.q_row0 - w.q_start) + r] = l > 0.f ? M + logf(l) : l == 0.f ? -INFINITY : l;
 }
 
 }  // namespace fa

@@ -21,12 +21,16 @@ constexpr int kWinBwdStages = D == 128 ? 2 : 4;
 template <int D, bool VARLEN, bool KPAD>
 cudaError_t launch_win(const WinLaunchArgs& a) {
   auto* kern = &fa_win_kernel<D, kWinStages<D>, VARLEN, KPAD>;
-  constexpr int smem = SmemLayout<D, 128, kWinStages<D>>::kAlloc;
+  constexpr int smem = WinSmem<D, kWinStages<D>>::kAlloc;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
-  const int grid = VARLEN ? a.p.num_units : std::min(a.p.num_units, a.num_sms);
+  const int grid = KPAD ? a.num_sms : VARLEN ? a.p.num_units : std::min(a.p.num_units, a.num_sms);
   kern<<<grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
+  if constexpr (KPAD) {
+    const dim3 rows(grid, (std::min(a.p.Nq, kBR * kQT) + 7) / 8);
+    fa_win_join_kernel<D, VARLEN><<<rows, 256, 0, a.stream>>>(a.p);
+  }
   return cudaGetLastError();
 }
 
@@ -107,6 +111,16 @@ BwdSizes bwd_sizes(int B, int Nq, int Nk, int H, int Hk, int d, int window, int 
 }
 
 }  // namespace
+
+size_t window_parts_bytes(int num_sms, int d) {
+  return static_cast<size_t>(num_sms) * (16 + 2 * kBR * kQT * (static_cast<size_t>(d) + 1) * 4);
+}
+
+void window_parts(WinParams& p, void* at, int num_sms) {
+  p.cut = static_cast<int2*>(at);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(at) + 16 * static_cast<size_t>(num_sms));
+  p.part_o = p.part_lse + static_cast<size_t>(num_sms) * 2 * kBR * kQT;
+}
 
 int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v, int Hk, int d, bool kpad) {
   WinParams& p = a.p;

@@ -19,4 +19,8 @@ struct WinLaunchArgs {
 // a length per sequence and Nk a multiple of 128.  Encodes the maps and launches.
 int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v, int Hk, int d, bool kpad);
 
+// kpad: the workspace for units cut between CTAs, 16-byte aligned.
+size_t window_parts_bytes(int num_sms, int d);
+void window_parts(WinParams& p, void* at, int num_sms);
+
 }  // namespace fa

@@ -83,11 +83,17 @@ HARNESS = r"""
 using std::min;
 static const int kBwdBK = 128, kBwdBQ = 128;
 %s
+struct WinSteps { int s, a, e; };
 %s
 extern "C" void query_blocks(int kb, int len_q, int len_k, int window, int sink, int* out) {
   win_query_blocks(kb, len_q, len_k, window, sink != 0, out[0], out[1]);
 }
-extern "C" int sees(int kt, int lo, int hi, int nsk) { return win_sees(kt, lo, hi, nsk); }
+extern "C" int sees(int lo, int hi, int nsk, int ns, int gap, int j) {
+  return win_sees(win_steps(lo, hi, nsk, ns, gap), j);
+}
+extern "C" int last(int lo, int hi, int nsk, int ns, int gap, int j0, int j1) {
+  return win_last(win_steps(lo, hi, nsk, ns, gap), j0, j1);
+}
 """
 
 
@@ -101,7 +107,8 @@ def _function(path, name):
 def test_blocks_walked_are_those_that_hold_a_visible_pair(tmp_path):
     """The index rules of the kernels, compiled for the host from their source, against the mask."""
     import ctypes
-    code = HARNESS % (_function("fa_win_bwd_kernel.cuh", "win_query_blocks("), _function("fa_win_kernel.cuh", "win_sees("))
+    code = HARNESS % (_function("fa_win_bwd_kernel.cuh", "win_query_blocks("), "".join(
+        _function("fa_win_kernel.cuh", name) for name in ("WinSteps win_steps(", "bool win_sees(")))
     (tmp_path / "w.cpp").write_text(code)
     so = str(tmp_path / "w.so")
     subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-o", so, str(tmp_path / "w.cpp")], check=True)
@@ -127,14 +134,31 @@ def test_blocks_walked_are_those_that_hold_a_visible_pair(tmp_path):
             assert set((rows // 128).tolist()) <= got
             if len(rows) and not sink:  # tight: no block without a visible pair but at the ends
                 assert len(got) <= len(set((rows // 128).tolist())) + 1
+        # Forward: the steps of a unit of two query tiles, and which of them each takes part in.
         nsk = -(-sinks // 128)
-        for t in range(-(-n_q // 128)):
-            r = np.arange(t * 128, min(n_q, t * 128 + 128)) + n_k - n_q
-            if r[-1] < 0:
+        for u in range(-(-n_q // 256)):
+            tiles = []
+            for t in (2 * u, 2 * u + 1):
+                r = np.arange(t * 128, min(n_q, t * 128 + 128)) + n_k - n_q
+                if len(r) and r[-1] >= 0:
+                    tiles.append((t, max(0, int(r[0]) - window + 1) // 128, int(r[-1]) // 128))
+            if not tiles:
                 continue
-            lo, hi = max(0, int(r[0]) - window + 1) // 128, int(r[-1]) // 128
-            for kt in range(-(-n_k // 128)):
-                any_seen = mask[t * 128:t * 128 + 128, kt * 128:kt * 128 + 128].any()
-                assert bool(lib.sees(kt, lo, hi, nsk)) >= bool(any_seen)
-                if not any_seen:
-                    assert not lib.sees(kt, lo, hi, nsk)
+            first, end = min(t[1] for t in tiles), max(t[2] for t in tiles)
+            ns = min(nsk, first)
+            gap = first - ns
+            steps = ns + end - first + 1
+            for t, lo, hi in tiles:
+                on = []
+                for j in range(steps):
+                    kt = j if j < ns else j + gap
+                    any_seen = bool(mask[t * 128:t * 128 + 128, kt * 128:kt * 128 + 128].any())
+                    assert bool(lib.sees(lo, hi, nsk, ns, gap, j)) == any_seen
+                    on.append(any_seen)
+                covered = [j if j < ns else j + gap for j in range(steps) if on[j]]
+                want = [kt for kt in range(-(-n_k // 128)) if mask[t * 128:t * 128 + 128, kt * 128:kt * 128 + 128].any()]
+                assert covered == want
+                for j0 in range(0, steps, 3):
+                    for j1 in (j0 + 1, steps):
+                        got = [j for j in range(j0, j1) if on[j]]
+                        assert lib.last(lo, hi, nsk, ns, gap, j0, j1) == (got[-1] if got else -1)
