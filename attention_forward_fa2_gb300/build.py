@@ -27,7 +27,7 @@ UNITS = ("fa_api.cu", "fa_fwd_d128.cu", "fa_fwd_d128_bc64.cu", "fa_fwd_d128_caus
          "fa_fwd_split.cu", "fa_static_scratch.cu", "fa_bwd.cu", "fa_fp8.cu",
          "fa_fp8_varlen.cu", "fa_window.cu", "fa_kv_append.cu", "fa_kv_attn.cu")
 HEADERS = ("ptx.cuh", "fa_fwd_kernel.cuh", "fa_launch.h", "fa_combine.cuh", "fa_bwd_kernel.cuh",
-           "fa_win_kernel.cuh", "fa_win_bwd_kernel.cuh", "fa_window.h", "fa_kvcache.h", "fa_kv_attn.cuh")
+           "fa_win_kernel.cuh", "fa_win_bwd_kernel.cuh", "fa_window.h", "fa_f16.cuh", "fa_kvcache.h", "fa_kv_attn.cuh")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

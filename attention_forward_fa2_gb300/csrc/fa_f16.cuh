@@ -1,0 +1,31 @@
+// fa_f16.cuh -- conversions through f16 shared by the cache and window kernels.
+#pragma once
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace fa {
+
+// Two floats to f16 (lo in bits 0-15) and back, as a packed pair of fp32.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint64_t unpack_f16x2(uint32_t v) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(v));
+  return ptx::f2_pack(lo, hi);
+}
+
+// Four e4m3 codes to two f16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+
+}  // namespace fa

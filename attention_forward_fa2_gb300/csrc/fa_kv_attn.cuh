@@ -42,6 +42,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "fa_f16.cuh"
 #include "fa_fwd_kernel.cuh"
 #include "fa_kvcache.h"
 #include "ptx.cuh"
@@ -132,19 +133,6 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams& p, int b) {
 }
 __device__ __forceinline__ long long kv_flat(const KvAttnParams& p, const KvSeq& s) {
   return static_cast<long long>(s.steps()) * s.units_per_head * p.Hk;
-}
-
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(v));
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // D (16 x 8, fp32) += A (16 x 16, f16) * B (16 x 8, f16).

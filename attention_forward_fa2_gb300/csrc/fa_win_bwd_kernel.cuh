@@ -25,11 +25,13 @@
 #include <cstdint>
 
 #include "fa_bwd_kernel.cuh"
+#include "fa_f16.cuh"
 #include "fa_win_kernel.cuh"
 #include "ptx.cuh"
 
 namespace fa {
 
+// BwdParams' lse2 and delta hold the negated values here.
 struct WinBwdParams : BwdParams {
   int window, sinks;
   int num_skb;         // key blocks that can hold sinks: ceil(min(sinks, Nk) / 128)
@@ -103,11 +105,12 @@ __device__ __forceinline__ WinBwdUnit win_bwd_decode(const WinBwdParams& p, int 
     w.kb = r % p.num_skb;
     r /= p.num_skb;
   } else {
+    // Key block by key block: under a long window the first blocks are seen by the
+    // most queries, and the round-robin over units of falling work stays even.
     w.chunk = -1;
-    const int rest = p.num_kb - p.num_skb;
     r = u - p.num_sink_units;
-    w.kb = p.num_skb + r % rest;
-    r /= rest;
+    w.kb = p.num_skb + r / (p.B * p.Hk);
+    r %= p.B * p.Hk;
   }
   w.hk = r % p.Hk;
   w.b = r / p.Hk;
@@ -350,9 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             issue_s(g + 1);
           }
-          // dK += dS^T Q, then dQ^T = K^T dS^T over dP.  Both read dS^T from shared
-          // memory: as dK's A operand it is K-major (key rows, queries along the
-          // 128-byte rows), as dQ^T's B operand MN-major.
+          // dK += dS^T Q, then dQ^T = K^T dS^T over dP, both from shared memory.  (dQ^T
+          // first, with dK under the drain, was measured 14 % slower; for d = 64, dQ^T
+          // in columns of its own no faster: what bounds the step is the chain of the
+          // softmax warps, 1.5 k cycles for P and 2.0 k for dS of 5.5 k, while the
+          // reductions of dQ, 64 KB a step, move 23 bytes a cycle for 2.8 k of them.)
           if (!wait(bar(L::kBarDSFull), g & 1u, kBSiteMmaDS)) break;
           ptx::tc_fence_after();
           const uint64_t qdesc_mn = ptx::sw128_desc(sq, L::kQPanel, 1024);
@@ -401,7 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool key_ok = r >= w.kw.lo && r < w.kw.hi;  // a key of this block
 #pragma unroll 1
       for (int i = 0; i < w.nsteps && ok; ++i, ++g) {
-        const int h = w.hk * p.group + i / w.nqb;
         const int qb = w.qb0 + i % w.nqb;
         // First query (sequence index) of this warpgroup's columns of the tile as loaded.
         const int q0 = make_window<VARLEN>(w.q_start, w.q_start + w.len_q, w.q_start + qb * kBwdBQ, kBwdBQ).load_row -
@@ -409,8 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Scaled LSE and D of this warpgroup's 64 queries, staged with Q(g)
         // (shared-memory broadcasts instead of dependent global loads).
         const uint32_t slot = g % STAGES;
-        const float4* l2g = reinterpret_cast<const float4*>(gbase + L::kOffLD + slot * L::kLDBytes) + c * 16;
-        const float4* dlg = l2g + kBwdBQ / 4;
+        // Pairs of -L log2 e, then of -D: the operands of the packed sums below.
+        const ulonglong2* l2g = reinterpret_cast<const ulonglong2*>(gbase + L::kOffLD + slot * L::kLDBytes) + c * 16;
+        const ulonglong2* dlg = l2g + kBwdBQ / 4;
         if (!ptx::mbar_wait_warp(bar(L::kBarSFull), g & 1u, s_abort, tmo) ||
             !ptx::mbar_wait_warp(bar(L::kBarQFull + slot), (g / STAGES) & 1u, s_abort, tmo)) {
           record_error(p.status, kErrTimeout, kBSiteSoftS);
@@ -422,12 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // not see the key (only tiles that hold a border are masked: the
         // diagonal, the window's end, the end of the sinks, keys of the next
         // block); the bf16 pairs of half hh go to columns 16 hh .. 16 hh + 15
-        // (already read).  The packed pairs stay in registers for dS: S(g + 1)
+        // (already read).  f16 pairs stay in registers for dS: S(g + 1)
         // overwrites these columns as soon as dV(g) has read them.
         const int q_pos = q0 + w.off;  // position of this warpgroup's first column
         const bool border = w.kw.lo != 0 || w.kw.hi != kBwdBK || kj0 + kBwdBK - 1 > q_pos ||
                             (kj0 <= q_pos + 63 - p.window && kj0 + kBwdBK > p.sinks);
-        uint32_t pk[32];
+        uint32_t ph[32];  // P^T in f16: its rounding (2^-11) does not add to that of dS
+        const uint64_t c2x2 = ptx::f2_pack(c2, c2);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           uint32_t sr[32];
@@ -435,17 +441,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_wait_ld();
           float e[32];
 #pragma unroll
-          for (int k4 = 0; k4 < 8; ++k4) {
-            const float4 l = l2g[hh * 8 + k4];
+          for (int k = 0; k < 32; k += 4) {
+            const ulonglong2 l = l2g[hh * 8 + k / 4];
 #pragma unroll
-            for (int k = 4 * k4; k < 4 * k4 + 4; k += 2) {
-              const float la = (k & 3) == 0 ? l.x : l.z, lb = (k & 3) == 0 ? l.y : l.w;
+            for (int h2 = 0; h2 < 2; ++h2) {
               float x0, x1;
-              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])),
-                                         ptx::f2_pack(c2, c2), ptx::f2_pack(-la, -lb)),
+              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(sr[k + 2 * h2]), __uint_as_float(sr[k + 2 * h2 + 1])),
+                                         c2x2, h2 == 0 ? l.x : l.y),
                              x0, x1);
-              e[k] = ptx::ex2(x0);
-              e[k + 1] = ptx::ex2(x1);
+              e[k + 2 * h2] = ptx::ex2(x0);
+              e[k + 2 * h2 + 1] = ptx::ex2(x1);
             }
           }
           if (border) {
@@ -459,13 +464,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((seen & (1u << k)) == 0u) e[k] = 0.f;
           }
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) pk[16 * hh + k / 2] = ptx::pack_bf16x2(e[k], e[k + 1]);
-          ptx::tmem_st16(tSc + hh * 16, &pk[16 * hh]);
+          for (int k = 0; k < 32; k += 2) ph[16 * hh + k / 2] = pack_f16x2(e[k], e[k + 1]);
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) pk[k / 2] = ptx::pack_bf16x2(e[k], e[k + 1]);
+          ptx::tmem_st16(tSc + hh * 16, pk);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(L::kBarPFull));
-        // dS^T = P^T o (dP^T - D), from the bf16 P^T pairs held above.
+        // dS^T = P^T o (dP^T - D), from the f16 P^T pairs held above.
         if (!ptx::mbar_wait_warp(bar(L::kBarDPFull), g & 1u, s_abort, tmo)) {
           record_error(p.status, kErrTimeout, kBSiteSoftDP);
           ok = false;
@@ -486,14 +494,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_ld32(tDc + hh * 32, dr);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int k4 = 0; k4 < 8; ++k4) {
-            const float4 dl = dlg[hh * 8 + k4];
+          for (int k = 0; k < 32; k += 4) {
+            const ulonglong2 dl = dlg[hh * 8 + k / 4];
 #pragma unroll
-            for (int k = 4 * k4; k < 4 * k4 + 4; k += 2) {
-              const float da = (k & 3) == 0 ? dl.x : dl.z, db = (k & 3) == 0 ? dl.y : dl.w;
-              const uint32_t pw = pk[16 * hh + k / 2];
-              const float p0 = __uint_as_float(pw << 16), p1 = __uint_as_float(pw & 0xffff0000u);
-              ds[k / 2] = ptx::pack_bf16x2(p0 * (__uint_as_float(dr[k]) - da), p1 * (__uint_as_float(dr[k + 1]) - db));
+            for (int h2 = 0; h2 < 2; ++h2) {
+              const int e = k + 2 * h2;
+              float y0, y1;
+              ptx::f2_unpack(ptx::f2_mul(ptx::f2_add(ptx::f2_pack(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1])),
+                                                     h2 == 0 ? dl.x : dl.y),
+                                         unpack_f16x2(ph[16 * hh + e / 2])),
+                             y0, y1);
+              ds[e / 2] = ptx::pack_bf16x2(y0, y1);
             }
           }
 #pragma unroll
@@ -618,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // lanes to a row, 16 bytes of bf16 a lane, and are bound by their bytes (the
 // accumulator's 4 d, and 4 d of o and dout, a row).
 //
-// D_i, the scaled log-sum-exp and a cleared accumulator row for every entry of
-// the tile order (see BwdParams): entries without a row of their own, and rows
-// without keys, carry lse2 = +inf, so that their P and dS are 0.
+// -D_i, the scaled log-sum-exp negated and a cleared accumulator row for every
+// entry of the tile order (see BwdParams): entries without a row of their own, and
+// rows without keys, carry -inf, so that their P and dS are 0.
 template <int D, bool VARLEN>
 __global__ void __launch_bounds__(256) fa_win_prep_kernel(const WinBwdParams p) {
   constexpr int kLanes = D / 8;
@@ -657,8 +668,8 @@ __global__ void __launch_bounds__(256) fa_win_prep_kernel(const WinBwdParams p) 
   for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
   if (!in) return;
   if (lane == 0) {
-    p.delta[row] = acc;
-    p.lse2[row] = l2;
+    p.delta[row] = -acc;
+    p.lse2[row] = -l2;
   }
   float* const dst = p.dq_acc + static_cast<size_t>(row) * D + lane * 4;
   ptx::st_global_v4(dst, 0u, 0u, 0u, 0u);

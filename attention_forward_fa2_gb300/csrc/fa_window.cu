@@ -94,16 +94,16 @@ struct BwdSizes {
   size_t dq_bytes, part_bytes;
 };
 
-// A chunk of a sink block walks about as many query blocks as the other units
-// (a window's worth and the two at its ends), at least 8 so that short windows
-// do not pay for many small chunks.
+// A chunk of a sink block walks as many query blocks as the other units do
+// (floor((window + 126) / 128) + 1), at least 4 so that short windows do not pay
+// for many small chunks.
 BwdSizes bwd_sizes(int B, int Nq, int Nk, int H, int Hk, int d, int window, int sinks) {
   BwdSizes z;
   const int blocks = (Nq + kBwdBQ - 1) / kBwdBQ;
   z.nq_pad = blocks * kBwdBQ;
   z.num_kb = (Nk + kBwdBK - 1) / kBwdBK;
   z.num_skb = (std::min(sinks, Nk) + kBwdBK - 1) / kBwdBK;
-  z.chunk_qb = std::max(8, std::min(window, std::max(Nk, 1)) / kBwdBQ + 2);
+  z.chunk_qb = std::max(4, (std::min(window, std::max(Nk, 1)) + 126) / kBwdBQ + 1);
   z.num_chunks = (blocks + z.chunk_qb - 1) / z.chunk_qb;
   z.dq_bytes = static_cast<size_t>(B) * H * z.nq_pad * (static_cast<size_t>(d) + 2) * 4;
   z.part_bytes = static_cast<size_t>(z.num_chunks) * B * Hk * z.num_skb * kBwdBK * 2 * d * 4;

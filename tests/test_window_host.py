@@ -47,7 +47,7 @@ def test_refusals(L, kw, code):
 def test_backward_workspace(L):
     def need(B, Nq, Nk, H, Hk, d, window, sinks):
         pad = -(-Nq // 128) * 128
-        chunk = max(8, min(window, max(Nk, 1)) // 128 + 2)
+        chunk = max(4, (min(window, max(Nk, 1)) + 126) // 128 + 1)
         chunks, skb = -(-pad // 128 // chunk) if pad else 0, -(-min(sinks, Nk) // 128)
         chunks = -(-(pad // 128) // chunk)
         return B * H * pad * (d + 2) * 4 + chunks * B * Hk * skb * 128 * 2 * d * 4
