@@ -87,6 +87,7 @@ struct WinParams {
   int group;                   // query heads per key/value head
   int window, sinks;
   int full;                    // 1: no causal border
+  int by_block;                // 1: units numbered query block by query block
   int num_mblocks;             // ceil(Nq / (kBR * kQT))
   int num_units;               // B * H * num_mblocks
   int total_q, total_k;        // variable-length form: packed rows (sequences past them are rejected)
@@ -122,10 +123,17 @@ __device__ __forceinline__ void win_restrict(WinUnit& w, int j0, int j1, int pla
 template <int BC, bool VARLEN, bool KPAD>
 __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
   WinUnit w;
-  // Packed batches: last query blocks first (under a long window the longest
-  // units), so that the running CTAs even out at the end.
-  const int mb = VARLEN ? p.num_mblocks - 1 - u % p.num_mblocks : u % p.num_mblocks;
-  const int r = u / p.num_mblocks;
+  // Head by head, so that the units in flight share keys in L2; packed batches
+  // last query blocks first (under a long window the longest units), so that the
+  // running CTAs even out at the end.  by_block (dense, windows over half the keys
+  // or more): the longest block of every head first, which keeps the round-robin
+  // over units of falling work even.
+  int mb = u % p.num_mblocks, r = u / p.num_mblocks;
+  if (p.by_block) {
+    mb = u / (p.B * p.H);
+    r = u % (p.B * p.H);
+  }
+  if (VARLEN || p.by_block) mb = p.num_mblocks - 1 - mb;
   w.h = r % p.H;
   w.b = r / p.H;
   w.hk = w.h / p.group;
@@ -620,20 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool border = kw.lo != 0 || kw.hi != BC || kbase + BC - 1 > pos_first ||
                             (kbase <= pos_last - p.window && kbase + BC > p.sinks);
         float s[BC];
-        // Border tiles: the row's visible columns as 32-bit words, [a, e) (window
-        // and diagonal) and [kw.lo, f) (sinks): a bit test and a select per score
-        // (four comparisons per score made a border tile cost several others).
-        uint32_t seen[BC / 32];
-        auto find_seen = [&]() {
-          const int e = min(kw.hi, pos - kbase + 1);
-          const int a = max(kw.lo, pos - p.window - kbase + 1);
-          const int f = min(e, p.sinks - kbase);
-#pragma unroll
-          for (int c = 0; c < BC / 32; ++c)
-            seen[c] = border ? (bits_below(e - 32 * c) & ~bits_below(a - 32 * c)) |
-                                   (bits_below(f - 32 * c) & ~bits_below(kw.lo - 32 * c))
-                             : ~0u;
-        };
         uint32_t pk[BC / 2];
         auto exp_range = [&](int c0, int c1, float ng, uint64_t (&acc)[4]) {
           const uint64_t c2x2 = ptx::f2_pack(c2, c2);
@@ -681,19 +675,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           slow = __any_sync(0xffffffffu, m_ref == -INFINITY || !(lblk <= accept_sum));
         }
         if (slow) {
-          {
-            uint32_t sr[BC];
+          uint32_t sr[BC];
 #pragma unroll
-            for (int c = 0; c < BC / 32; ++c) ptx::tmem_ld32(tS + c * 32, &sr[c * 32]);
-            find_seen();
-            ptx::tmem_wait_ld();
+          for (int c = 0; c < BC / 32; ++c) ptx::tmem_ld32(tS + c * 32, &sr[c * 32]);
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < BC; ++c) s[c] = __uint_as_float(sr[c]);
-          }
+          for (int c = 0; c < BC; ++c) s[c] = __uint_as_float(sr[c]);
           if (border) {
+            // The row's visible columns as 32-bit words, [a, e) (window and diagonal)
+            // and [kw.lo, f) (sinks): a bit test and a select per score (four
+            // comparisons per score made a border tile cost several others).
+            const int e = min(kw.hi, pos - kbase + 1);
+            const int a = max(kw.lo, pos - p.window - kbase + 1);
+            const int f = min(e, p.sinks - kbase);
 #pragma unroll
-            for (int c = 0; c < BC; ++c)
-              if ((seen[c / 32] & (1u << (c % 32))) == 0u) s[c] = -INFINITY;
+            for (int c0 = 0; c0 < BC; c0 += 32) {
+              const uint32_t seen = (bits_below(e - c0) & ~bits_below(a - c0)) | (bits_below(f - c0) & ~bits_below(kw.lo - c0));
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if ((seen & (1u << c)) == 0u) s[c0 + c] = -INFINITY;
+            }
           }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll

@@ -141,6 +141,7 @@ int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v,
   // the kernel's index arithmetic stays in 32 bits.
   p.window = std::min(p.window, std::max(p.Nk, 1));
   p.sinks = std::min(p.sinks, p.Nk);
+  p.by_block = !varlen && !kpad && p.window >= p.Nk / 2;
   p.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
   // A row's first tile may show it a single key (the window's start, few sinks),
   // so its reference maximum is often far below its true one.  Nothing is lost
