@@ -136,12 +136,14 @@ __device__ __forceinline__ void unpack_e4m3x2(uint32_t codes, float& lo, float& 
 }
 
 // THREADS = 32: an item is a warp's (few new tokens); 256: a block's.
-// ITERS rows per group of lanes; THREADS / (D / 8) * ITERS rows hold an item's.
-template <int D, int THREADS, int ITERS, bool INTER>
-__global__ void __launch_bounds__(256) fa_kv_append_kernel(const AppendParams p) {
+// ITERS rows per group of lanes; THREADS / (D / 8) * ITERS rows hold a page's.
+// HEADS heads of a page are one item: their loads are in flight together, and the
+// angles of a row are loaded once for all of them.
+template <int D, int THREADS, int ITERS, int HEADS, bool INTER>
+__global__ void __launch_bounds__(256, THREADS > 32 ? 3 : ITERS > 1 ? 2 : 4) fa_kv_append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 8;            // lanes of a row
   constexpr int kRows = THREADS / kLanes;  // rows per iteration of an item
-  __shared__ uint32_t s_max[8];
+  __shared__ uint32_t s_max[8][HEADS];
   const int b = blockIdx.x / (p.kv_blocks + p.q_blocks);
   const int r = blockIdx.x % (p.kv_blocks + p.q_blocks);
   const int c = threadIdx.x % kLanes;
@@ -153,24 +155,25 @@ __global__ void __launch_bounds__(256) fa_kv_append_kernel(const AppendParams p)
     return;
   }
   if (r >= p.kv_blocks) {
-    // ------------------------------------------------- queries: 4 heads of a token per group of lanes
+    // ------------------------- queries: QHEADS heads of a token per group of lanes
+    constexpr int kQHeads = THREADS > 32 ? 8 : 4;
     constexpr int kGroups = 256 / kLanes;
-    const int quads = (p.H + 3) >> 2;
+    const int sets = (p.H + kQHeads - 1) / kQHeads;
     const long long item = static_cast<long long>(r - p.kv_blocks) * kGroups + threadIdx.x / kLanes;
-    const bool in = item < static_cast<long long>(n) * quads;
-    const int i = in ? static_cast<int>(item / quads) : 0;
-    const int h0 = in ? 4 * static_cast<int>(item % quads) : 0;
+    const bool in = item < static_cast<long long>(n) * sets;
+    const int i = in ? static_cast<int>(item / sets) : 0;
+    const int h0 = in ? kQHeads * static_cast<int>(item % sets) : 0;
     const __nv_bfloat16* src = p.q + static_cast<size_t>(row0 + i) * p.q_stride + static_cast<size_t>(h0) * D + 8 * c;
-    uint4 raw[4];
+    uint4 raw[kQHeads];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < kQHeads; ++e)
       raw[e] = in && h0 + e < p.H ? *reinterpret_cast<const uint4*>(src + e * D) : make_uint4(0, 0, 0, 0);
     Turn t;
     const bool turns = in && 8 * c < p.rot;
     if (turns) load_turn<INTER>(p, old_len + i, c, t);
     __nv_bfloat16* dst = p.q_out + (static_cast<size_t>(row0 + i) * p.H + h0) * D + 8 * c;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kQHeads; ++e) {
       float x[8];
       unpack8(raw[e], x);
       if (!INTER || turns) rotate8<INTER>(p, c, raw[e], t, x);
@@ -186,10 +189,11 @@ __global__ void __launch_bounds__(256) fa_kv_append_kernel(const AppendParams p)
   }
   // ------------------------------------------------------------ a page of one head of K or V
   const int item = r * (256 / THREADS) + (THREADS == 32 ? threadIdx.x >> 5 : 0);
-  if (item >= p.touch * p.Hk * 2) return;  // whole warps (THREADS = 32) or the whole block
+  const int head_groups = (p.Hk + HEADS - 1) / HEADS;
+  if (item >= p.touch * head_groups * 2) return;  // whole warps (THREADS = 32) or the whole block
   const bool is_k = (item & 1) == 0;
-  const int hk = (item >> 1) % p.Hk;
-  const int pg = old_len / p.page + (item >> 1) / p.Hk;  // page of the sequence
+  const int h0 = (item >> 1) % head_groups * HEADS;
+  const int pg = old_len / p.page + (item >> 1) / head_groups;  // page of the sequence
   // Slots [s0, s1) of the page take new tokens.
   const int s0 = max(old_len - pg * p.page, 0);
   const int s1 = min(old_len + n - pg * p.page, p.page);
@@ -199,106 +203,137 @@ __global__ void __launch_bounds__(256) fa_kv_append_kernel(const AppendParams p)
     if (threadIdx.x % THREADS == 0) record_error(p.status, kErrBadPage, 0);
     return;
   }
-  const size_t ph = static_cast<size_t>(id) * p.Hk + hk;
-  float* const scale_ptr = (is_k ? p.k_scale : p.v_scale) + ph;
-  uint8_t* const codes = (is_k ? p.k8 : p.v8) + ph * p.page * D;
-  const float old_scale = s0 > 0 ? *scale_ptr : 0.f;
+  const size_t ph0 = static_cast<size_t>(id) * p.Hk + h0;
+  float* const scales = (is_k ? p.k_scale : p.v_scale) + ph0;
+  uint8_t* const codes = (is_k ? p.k8 : p.v8) + ph0 * p.page * D;
   const int tid = threadIdx.x % THREADS;
   const __nv_bfloat16* const x0 = is_k ? p.k : p.v;
   const long long stride = is_k ? p.k_stride : p.v_stride;
   const bool turn_item = is_k && p.rot > 0;
-  float x[ITERS][8];
-  uint32_t amax = 0;
+  float old_scale[HEADS];
+#pragma unroll
+  for (int g = 0; g < HEADS; ++g) old_scale[g] = s0 > 0 && h0 + g < p.Hk ? scales[g] : 0.f;
+  // The rows stay in registers as they were read (rotated keys would take twice the
+  // registers); keys are rotated once for the maximum and once for the codes.
+  uint4 raw[HEADS][ITERS];
+  uint32_t amax[HEADS];
 #pragma unroll
   for (int it = 0; it < ITERS; ++it) {
     const int slot = s0 + it * kRows + tid / kLanes;
-    const bool in = slot < s1;
-    const int i = pg * p.page + slot - old_len;  // index among the new tokens
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (in) raw = *reinterpret_cast<const uint4*>(x0 + static_cast<size_t>(row0 + i) * stride + hk * D + 8 * c);
-    unpack8(raw, x[it]);
-    if (turn_item) {
+    const int i = slot < s1 ? pg * p.page + slot - old_len : 0;  // index among the new tokens
+    const __nv_bfloat16* const src = x0 + static_cast<size_t>(row0 + i) * stride + h0 * D + 8 * c;
+#pragma unroll
+    for (int g = 0; g < HEADS; ++g)
+      raw[g][it] = slot < s1 && h0 + g < p.Hk ? *reinterpret_cast<const uint4*>(src + g * D) : make_uint4(0, 0, 0, 0);
+  }
+  // Calls f(g, it, values) for every row, in fp32 and rotated.
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) {
+      const int slot = s0 + it * kRows + tid / kLanes;
+      const bool turns = turn_item && slot < s1 && 8 * c < p.rot;
       Turn t;
-      const bool turns = in && 8 * c < p.rot;
-      if (turns) load_turn<INTER>(p, old_len + i, c, t);
-      float y[8];
+      if (turns) load_turn<INTER>(p, pg * p.page + slot, c, t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[it][e];
-      if (!INTER || turns) rotate8<INTER>(p, c, raw, t, y);
-      if (turns) {
+      for (int g = 0; g < HEADS; ++g) {
+        float y[8];
+        unpack8(raw[g][it], y);
+        if (turn_item) {
+          float z[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[it][e] = y[e];
+          for (int e = 0; e < 8; ++e) z[e] = y[e];
+          if (!INTER || turns) rotate8<INTER>(p, c, raw[g][it], t, z);
+          if (turns) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = z[e];
+          }
+        }
+        f(g, slot, y);
       }
     }
-    amax = amax8(x[it], amax);
-  }
-  amax = __reduce_max_sync(0xffffffffu, amax);
+  };
+#pragma unroll
+  for (int g = 0; g < HEADS; ++g) amax[g] = 0u;
+  each([&](int g, int, const float(&y)[8]) { amax[g] = amax8(y, amax[g]); });
+#pragma unroll
+  for (int g = 0; g < HEADS; ++g) amax[g] = __reduce_max_sync(0xffffffffu, amax[g]);
   if constexpr (THREADS > 32) {
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int g = 0; g < HEADS; ++g) s_max[threadIdx.x >> 5][g] = amax[g];
+    }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) amax = max(amax, s_max[w]);
-  }
-  const float need = __uint_as_float(static_cast<uint32_t>(kv_scale_exp(amax) + 127) << 23);
-  const float scale = fmaxf(old_scale, need);
-  const float inv = 1.f / scale;  // exact
-  if (s0 > 0 && scale > old_scale) {
-    const float ratio = old_scale * inv;
-    for (int e = tid; e < s0 * (D / 16); e += THREADS) {
-      uint4* const ptr = reinterpret_cast<uint4*>(codes) + e;
-      const uint4 w = *ptr;
-      uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    for (int g = 0; g < HEADS; ++g)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float a, d0, d1, d2;
-        unpack_e4m3x2(v[k], a, d0);
-        unpack_e4m3x2(v[k] >> 16, d1, d2);
-        v[k] = pack4(a * ratio, d0 * ratio, d1 * ratio, d2 * ratio);
+      for (int w = 0; w < THREADS / 32; ++w) amax[g] = max(amax[g], s_max[w][g]);
+  }
+  float inv[HEADS];
+#pragma unroll
+  for (int g = 0; g < HEADS; ++g) {
+    const float need = __uint_as_float(static_cast<uint32_t>(kv_scale_exp(amax[g]) + 127) << 23);
+    const float scale = fmaxf(old_scale[g], need);
+    inv[g] = 1.f / scale;  // exact
+    if (h0 + g >= p.Hk) continue;
+    if (s0 > 0 && scale > old_scale[g]) {
+      const float ratio = old_scale[g] * inv[g];
+      for (int e = tid; e < s0 * (D / 16); e += THREADS) {
+        uint4* const ptr = reinterpret_cast<uint4*>(codes + static_cast<size_t>(g) * p.page * D) + e;
+        const uint4 w = *ptr;
+        uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a, d0, d1, d2;
+          unpack_e4m3x2(v[k], a, d0);
+          unpack_e4m3x2(v[k] >> 16, d1, d2);
+          v[k] = pack4(a * ratio, d0 * ratio, d1 * ratio, d2 * ratio);
+        }
+        *ptr = make_uint4(v[0], v[1], v[2], v[3]);
       }
-      *ptr = make_uint4(v[0], v[1], v[2], v[3]);
     }
+    if (tid == 0) scales[g] = scale;
   }
-#pragma unroll
-  for (int it = 0; it < ITERS; ++it) {
-    const int slot = s0 + it * kRows + tid / kLanes;
-    if (slot < s1) {
-      const float(&y)[8] = x[it];
-      *reinterpret_cast<uint2*>(codes + static_cast<size_t>(slot) * D + 8 * c) =
-          make_uint2(pack4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                     pack4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-    }
-  }
-  if (tid == 0) *scale_ptr = scale;
+  each([&](int g, int slot, const float(&y)[8]) {
+    if (slot < s1 && h0 + g < p.Hk)
+      *reinterpret_cast<uint2*>(codes + (static_cast<size_t>(g) * p.page + slot) * D + 8 * c) =
+          make_uint2(pack4(y[0] * inv[g], y[1] * inv[g], y[2] * inv[g], y[3] * inv[g]),
+                     pack4(y[4] * inv[g], y[5] * inv[g], y[6] * inv[g], y[7] * inv[g]));
+  });
 }
 
-template <int D, int THREADS, int ITERS>
+template <int D, int THREADS, int ITERS, int HEADS>
 void launch(AppendParams& p, bool inter, cudaStream_t stream) {
-  const int items = p.touch * p.Hk * 2;
+  const int items = p.touch * ((p.Hk + HEADS - 1) / HEADS) * 2;
   p.kv_blocks = THREADS == 32 ? (items + 7) / 8 : items;
-  const long long groups = static_cast<long long>(p.max_new) * ((p.H + 3) / 4);
+  constexpr int kQHeads = THREADS > 32 ? 8 : 4;
+  const long long groups = static_cast<long long>(p.max_new) * ((p.H + kQHeads - 1) / kQHeads);
   p.q_blocks = p.q ? static_cast<int>((groups + 256 / (D / 8) - 1) / (256 / (D / 8))) : 0;
   const unsigned grid = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.kv_blocks + p.q_blocks);
   if (inter)
-    fa_kv_append_kernel<D, THREADS, ITERS, true><<<grid, 256, 0, stream>>>(p);
+    fa_kv_append_kernel<D, THREADS, ITERS, HEADS, true><<<grid, 256, 0, stream>>>(p);
   else
-    fa_kv_append_kernel<D, THREADS, ITERS, false><<<grid, 256, 0, stream>>>(p);
+    fa_kv_append_kernel<D, THREADS, ITERS, HEADS, false><<<grid, 256, 0, stream>>>(p);
 }
 
-// Few new tokens (at most 8 rows of d = 128, 16 of d = 64): an item per warp.
+// Few new tokens (up to 2 or 8 rows of d = 128, 4 or 16 of d = 64): an item per warp and
+// head, so that a batch of single tokens spreads over the SMs.  More: a block per
+// page and up to four heads, whose loads cover one another's latency.
 template <int D>
 void dispatch(AppendParams& p, bool inter, cudaStream_t stream) {
   constexpr int kRows = 256 / (D / 8);
   const int rows = std::min(p.page, p.max_new);
-  if (rows <= 4 * (kRows / 8))
-    launch<D, 32, 4>(p, inter, stream);
+  if (rows <= kRows / 8)
+    launch<D, 32, 1, 1>(p, inter, stream);
+  else if (rows <= 4 * (kRows / 8))
+    launch<D, 32, 4, 1>(p, inter, stream);
   else if (rows <= kRows)
-    launch<D, 256, 1>(p, inter, stream);
+    launch<D, 256, 1, 4>(p, inter, stream);
   else if (rows <= 2 * kRows)
-    launch<D, 256, 2>(p, inter, stream);
+    launch<D, 256, 2, 4>(p, inter, stream);
   else if (rows <= 4 * kRows)
-    launch<D, 256, 4>(p, inter, stream);
+    launch<D, 256, 4, 2>(p, inter, stream);
   else
-    launch<D, 256, 8>(p, inter, stream);  // page 128 at d = 128
+    launch<D, 256, 8, 1>(p, inter, stream);  // page 128 at d = 128
 }
 
 }  // namespace
