@@ -17,6 +17,7 @@ forms) run the forward on block-quantised e4m3 inputs (§15.5).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -679,8 +680,20 @@ def forward_fp8(t, scale=None, causal=False, out=None, lse=None, stream=None):
 
 
 # The cache and window entries serve single tokens, where a call's host time is what
-# counts: their checks read each attribute once, and the slow, telling form of a check
-# runs only to raise.
+# counts: their checks read each attribute once, the slow, telling form of a check runs
+# only to raise, and torch's names are looked up once (torch is imported with the first
+# call, so that the library can be built without it).
+_torch = _current_device = _raw_stream = None
+
+
+def _import_torch():
+    global _torch, _current_device, _raw_stream
+    import torch
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _torch = torch
+    return torch
+
+
 def _dense(name, t, dtype, ndim, device):
     """t is a contiguous tensor of this type, rank and device (else raises); its address."""
     try:
@@ -693,7 +706,7 @@ def _dense(name, t, dtype, ndim, device):
 
 
 def _cuda_device(name, t):
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
@@ -704,23 +717,20 @@ def _cuda_device(name, t):
 def _stream_scope(stream, t):
     """Makes `stream` current: what the call allocates then belongs to it, and is not handed to
     another stream's work while this one's kernels run."""
-    import torch
     if _cuda_device("the first tensor", t) != stream.device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
-    return torch.cuda.stream(stream)
+    return _torch.cuda.stream(stream)
 
 
 def _launch(entry, device, args):
     """Call a C entry (its last argument is the stream) on the current stream of `device`."""
-    from torch import _C
     index = device.index
     fn = getattr(_lib or lib(), entry)
-    if index == _C._cuda_getDevice():
-        rc = fn(*args, _C._cuda_getCurrentRawStream(index))
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
-        import torch
-        with torch.cuda.device(device):
-            rc = fn(*args, _C._cuda_getCurrentRawStream(index))
+        with _torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(index))
     if rc != FA_OK:
         raise FaError(rc, entry)
 
@@ -728,11 +738,10 @@ def _launch(entry, device, args):
 def _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale):
     """Checked arguments of the window entries: (device, addresses of q, k, v, (B, Nq, Nk, H, Hk,
     d, scale), (cu_q, cu_k, total_q, total_k))."""
-    import torch
     packed = cu_seqlens_q is not None or cu_seqlens_k is not None
     device = _cuda_device("q", q)
-    ndim = 3 if packed else 4
-    ptrs = tuple(_dense(name, t, torch.bfloat16, ndim, device) for name, t in (("q", q), ("k", k), ("v", v)))
+    ndim, bf16 = 3 if packed else 4, _torch.bfloat16
+    ptrs = _dense("q", q, bf16, ndim, device), _dense("k", k, bf16, ndim, device), _dense("v", v, bf16, ndim, device)
     qs, ks = q.shape, k.shape
     H, d = qs[-2:]
     Hk = ks[-2]
@@ -745,8 +754,8 @@ def _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqle
         return device, ptrs, (qs[0], qs[1], ks[1], H, Hk, d, scale), (None, None, 0, 0)
     if cu_seqlens_q is None or cu_seqlens_k is None or max_seqlen_q is None or max_seqlen_k is None:
         raise ValueError("packed sequences need cu_seqlens_q/k and max_seqlen_q/k")
-    cu = (_dense("cu_seqlens_q", cu_seqlens_q, torch.int32, 1, device),
-          _dense("cu_seqlens_k", cu_seqlens_k, torch.int32, 1, device))
+    cu = (_dense("cu_seqlens_q", cu_seqlens_q, _torch.int32, 1, device),
+          _dense("cu_seqlens_k", cu_seqlens_k, _torch.int32, 1, device))
     B = cu_seqlens_q.numel() - 1
     if B < 0 or cu_seqlens_k.numel() != B + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k need B + 1 entries each")
@@ -760,9 +769,8 @@ def _int32(x):
 
 def _out_like(name, t, like, device):
     """An output tensor of the caller's, checked, or a new one like `like`."""
-    import torch
     if t is None:
-        return torch.empty_like(like)
+        return _torch.empty_like(like)
     _dense(name, t, like.dtype, like.dim(), device)
     if t.shape != like.shape:
         raise ValueError("%s shape mismatch" % name)
@@ -770,10 +778,9 @@ def _out_like(name, t, like, device):
 
 
 def _lse_out(lse, shape, device):
-    import torch
     if lse is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
-    _dense("lse", lse, torch.float32, 3, device)
+        return _torch.empty(shape, dtype=_torch.float32, device=device)
+    _dense("lse", lse, _torch.float32, 3, device)
     if lse.shape != shape:
         raise ValueError("lse must be %s" % (tuple(shape),))
     return lse
@@ -781,11 +788,10 @@ def _lse_out(lse, shape, device):
 
 def _workspace(t, need, device):
     """The caller's workspace, checked, or a new one: (address, bytes, tensor)."""
-    import torch
     if t is None:
         if need == 0:
             return None, 0, None
-        t = torch.empty(need, dtype=torch.uint8, device=device)
+        t = _torch.empty(need, dtype=_torch.uint8, device=device)
         return t.data_ptr(), need, t
     if t.device != device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % (device,))
@@ -817,13 +823,12 @@ def forward_window(q, k, v, window, sinks=0, scale=None, cu_seqlens_q=None, cu_s
 def backward_window(q, k, v, o, lse, dout, window, sinks=0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None,
                     max_seqlen_q=None, max_seqlen_k=None, workspace=None, dq=None, dk=None, dv=None, stream=None):
     """Gradients (dq, dk, dv) of forward_window given dout = dL/dO and its o and lse."""
-    import torch
     if stream is not None:
         with _stream_scope(stream, q):
             return backward_window(q, k, v, o, lse, dout, window, sinks, scale, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                                    max_seqlen_k, workspace, dq, dk, dv)
     device, ptrs, sizes, cu = _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
-    more = tuple(_dense(name, t, torch.bfloat16, q.dim(), device) for name, t in (("o", o), ("dout", dout)))
+    more = tuple(_dense(name, t, _torch.bfloat16, q.dim(), device) for name, t in (("o", o), ("dout", dout)))
     if o.shape != q.shape or dout.shape != q.shape:
         raise ValueError("o and dout must have q's shape")
     B, Nq, Nk, H, Hk, d = sizes[:6]
@@ -845,11 +850,10 @@ class KvCache:
     Code c of a page and head stands for c * scale."""
 
     def __init__(self, k8, v8, k_scale, v_scale):
-        import torch
         self.device = device = _cuda_device("k8", k8)
-        self._codes = _dense("k8", k8, torch.uint8, 4, device), _dense("v8", v8, torch.uint8, 4, device)
-        self._scales = (_dense("k_scale", k_scale, torch.float32, 2, device),
-                        _dense("v_scale", v_scale, torch.float32, 2, device))
+        self._codes = _dense("k8", k8, _torch.uint8, 4, device), _dense("v8", v8, _torch.uint8, 4, device)
+        self._scales = (_dense("k_scale", k_scale, _torch.float32, 2, device),
+                        _dense("v_scale", v_scale, _torch.float32, 2, device))
         shape = k8.shape
         if v8.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
             raise ValueError("codes are [num_pages, Hk, page, d], scales [num_pages, Hk]")
@@ -859,29 +863,31 @@ class KvCache:
     @classmethod
     def empty(cls, num_pages, page, Hk, d, device="cuda"):
         """A cache of unwritten pages (append_kvcache sets a page's scale with its first token)."""
-        import torch
-        codes = [torch.zeros((num_pages, Hk, page, d), dtype=torch.uint8, device=device) for _ in range(2)]
-        scales = [torch.zeros((num_pages, Hk), dtype=torch.float32, device=device) for _ in range(2)]
+        torch = _torch or _import_torch()
+        codes = [torch.zeros((num_pages, Hk, page, d), dtype=_torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros((num_pages, Hk), dtype=_torch.float32, device=device) for _ in range(2)]
         return cls(*codes, *scales)
 
 
 def _token_rows(name, t, ndim, device):
     """Address of t [B, n, heads, d] or [total, heads, d], and the distance in elements between its
     token rows."""
-    import torch
     try:
-        fine = t.dtype is torch.bfloat16 and t.device == device and t.dim() == ndim
+        fine = t.dtype is _torch.bfloat16 and t.device == device and t.dim() == ndim
     except AttributeError:
         fine = False
     if not fine:
         _cuda_device(name, t)
-        if t.dtype != torch.bfloat16:
-            raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+        if t.dtype != _torch.bfloat16:
+            raise TypeError("%s must be %s, got %s" % (name, _torch.bfloat16, t.dtype))
         if t.dim() != ndim:
             raise ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    shape, s = t.shape, t.stride()
+    shape = t.shape
     heads, d = shape[-2:]
+    if t.is_contiguous():
+        return t.data_ptr(), heads * d
+    s = t.stride()
     if (d > 1 and s[-1] != 1) or (heads > 1 and s[-2] != d):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     if ndim == 3:
@@ -894,8 +900,7 @@ def _token_rows(name, t, ndim, device):
 
 def _sequences(name, lens, block_table, B, device):
     """Addresses of the lengths and the table, and the table's width."""
-    import torch
-    ptr, table = _dense(name, lens, torch.int32, 1, device), _dense("block_table", block_table, torch.int32, 2, device)
+    ptr, table = _dense(name, lens, _torch.int32, 1, device), _dense("block_table", block_table, _torch.int32, 2, device)
     if lens.shape[0] != B:
         raise ValueError("%s needs %d entries" % (name, B))
     rows, width = block_table.shape
@@ -915,7 +920,6 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
     no rotation; pairs are halves, or neighbours when interleaved.  q: [.., H, d] with
     k's tokens.  Returns the rotated q (q_out or a new contiguous tensor), None
     without q."""
-    import torch
     if stream is not None:
         with _stream_scope(stream, k):
             return append_kvcache(cache, k, v, block_table, cache_lens, q, cos, sin, interleaved, cu_seqlens, max_seqlen,
@@ -931,7 +935,7 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
         raise ValueError("k, v and the cache differ in shape")
     cu = None
     if packed:
-        cu = _dense("cu_seqlens", cu_seqlens, torch.int32, 1, device)
+        cu = _dense("cu_seqlens", cu_seqlens, _torch.int32, 1, device)
         if max_seqlen is None:
             raise ValueError("max_seqlen is required with cu_seqlens")
         B, total, n = cu_seqlens.shape[0] - 1, shape[0], int(max_seqlen)
@@ -944,7 +948,7 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
     rot = max_pos = 0
     cp = sp = None
     if cos is not None:
-        cp, sp = _dense("cos", cos, torch.float32, 2, device), _dense("sin", sin, torch.float32, 2, device)
+        cp, sp = _dense("cos", cos, _torch.float32, 2, device), _dense("sin", sin, _torch.float32, 2, device)
         if sin.shape != cos.shape:
             raise ValueError("cos and sin differ in shape")
         max_pos, rot = cos.shape
@@ -958,10 +962,10 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
             raise ValueError("q and k differ in their tokens")
         H = qs[-2]
         if q_out is None:
-            q_out = torch.empty(qs, dtype=torch.bfloat16, device=device)
+            q_out = _torch.empty(qs, dtype=_torch.bfloat16, device=device)
             qop = q_out.data_ptr()
         else:
-            qop = _dense("q_out", q_out, torch.bfloat16, ndim, device)
+            qop = _dense("q_out", q_out, _torch.bfloat16, ndim, device)
             if q_out.shape != qs:
                 raise ValueError("q_out shape mismatch")
     elif q_out is not None:
@@ -972,6 +976,13 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
+def _kv_need(index, *sizes):
+    """kvcache_workspace_bytes on device `index` (the plan depends on its SM count)."""
+    with _torch.cuda.device(index):
+        return kvcache_workspace_bytes(*sizes)
+
+
 def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, causal=True, window=0, sinks=0,
                     cu_seqlens_q=None, max_seqlen_q=None, workspace=None, out=None, lse=None, stream=None):
     """Attention over a paged e4m3 cache.
@@ -980,14 +991,13 @@ def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, c
     seq_lens: int32 [B], tokens of each sequence (the queries' own included), at most
     max_seqlen_k.  causal: query i of n stands at position seq_lens - n + i; window
     (0: none) and sinks as forward_window.  Returns (o like q, lse fp32 [B, H, n])."""
-    import torch
     if stream is not None:
         with _stream_scope(stream, q):
             return forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale, causal, window, sinks,
                                    cu_seqlens_q, max_seqlen_q, workspace, out, lse)
     packed = cu_seqlens_q is not None
     device = cache.device
-    qp = _dense("q", q, torch.bfloat16, 3 if packed else 4, device)
+    qp = _dense("q", q, _torch.bfloat16, 3 if packed else 4, device)
     shape = q.shape
     H, d = shape[-2:]
     Hk = cache.Hk
@@ -997,7 +1007,7 @@ def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, c
         raise ValueError("query heads (%d) must be a multiple of key/value heads (%d)" % (H, Hk))
     cu = None
     if packed:
-        cu = _dense("cu_seqlens_q", cu_seqlens_q, torch.int32, 1, device)
+        cu = _dense("cu_seqlens_q", cu_seqlens_q, _torch.int32, 1, device)
         if max_seqlen_q is None:
             raise ValueError("max_seqlen_q is required with cu_seqlens_q")
         B, n, total = cu_seqlens_q.shape[0] - 1, int(max_seqlen_q), shape[0]
@@ -1009,9 +1019,8 @@ def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, c
     causal, window, sinks, max_k = 1 if causal else 0, _int32(window), _int32(sinks), int(max_seqlen_k)
     out = _out_like("out", out, q, device)
     lse = _lse_out(lse, (B, H, n), device)
-    with _on_device(device):  # the plan depends on the device's SM count
-        need = kvcache_workspace_bytes(B, n, max_k, H, Hk, d, causal, window, sinks)
-    ws, ws_bytes, workspace = _workspace(workspace, need, device)
+    ws, ws_bytes, workspace = _workspace(workspace, _kv_need(device.index, B, n, max_k, H, Hk, d, causal, window, sinks),
+                                         device)
     _launch("fa_fwd_kvcache", device,
             (qp, *cache._codes, *cache._scales, table, lens, cu, out.data_ptr(), lse.data_ptr(), B, total, n, max_k, H, Hk,
              d, cache.page, cache.num_pages, width, scale, causal, window, sinks, ws, ws_bytes))
