@@ -16,13 +16,14 @@ namespace fa {
 namespace {
 
 // Query rows per key/value head (queries times heads of a group) up to which the
-// kernel for few rows runs, a unit of 16 rows at a time (the codes of later row
+// kernel for few rows runs, a unit of 8 or 16 rows at a time (the codes of later row
 // groups come from L2); above, the query chunk is long enough for 128-row tcgen05
 // tiles.
 constexpr int kFewRows = 64;
 
 struct KvPlan {
   bool few;
+  int rows;             // few rows: query rows per unit
   int ctas;             // few rows: CTAs (at most three an SM; fewer when there are fewer steps)
   int k_pad;            // chunk form: key rows per sequence of the bf16 copy
   size_t ws_bytes;
@@ -43,9 +44,10 @@ KvPlan kv_plan(int B, int max_q, int max_k, int H, int Hk, int d, int causal, in
     const long long win = (static_cast<long long>(window) + max_q + kKvTile - 2) / kKvTile + 1;
     steps = std::min(steps, win + (static_cast<long long>(sinks) + kKvTile - 1) / kKvTile);
   }
-  const long long all = B * static_cast<long long>(Hk) * ((rows + kKvRows - 1) / kKvRows) * std::max<long long>(steps, 1);
+  z.rows = rows <= 8 ? 8 : 16;
+  const long long all = B * static_cast<long long>(Hk) * ((rows + z.rows - 1) / z.rows) * std::max<long long>(steps, 1);
   z.ctas = static_cast<int>(std::max<long long>(1, std::min<long long>(all, kKvCtasPerSm * num_sms)));
-  z.ws_bytes = static_cast<size_t>(z.ctas) * (16 + 2 * kKvRows * (static_cast<size_t>(d) + 1) * 4);
+  z.ws_bytes = static_cast<size_t>(z.ctas) * (16 + 2 * z.rows * (static_cast<size_t>(d) + 1) * 4);
   return z;
 }
 
@@ -58,16 +60,16 @@ int encode_cache(CUtensorMap* m, const void* codes, long long rows, int d, int p
                      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const KvAttnParams& p, int ctas, cudaStream_t stream) {
-  auto* kern = &fa_kv_attn_kernel<D>;
-  constexpr int smem = KvSmem<D>::kAlloc;
+  auto* kern = &fa_kv_attn_kernel<D, NT>;
+  constexpr int smem = KvSmem<D, NT>::kAlloc;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kKvThreads, smem, stream>>>(tk, tv, p);
-  const dim3 grid(ctas, std::min(kKvRows, p.max_q * p.G));
-  fa_kv_join_kernel<D><<<grid, 128, 0, stream>>>(p);
+  const dim3 grid(ctas, std::min(8 * NT, p.max_q * p.G));
+  fa_kv_join_kernel<D, 8 * NT><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -224,7 +226,7 @@ int fa_fwd_kvcache(const void* q, const void* k8, const void* v8, const float* k
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.cut = static_cast<int4*>(workspace);
     p.part_lse = reinterpret_cast<float*>(p.cut + z.ctas);
-    p.part_o = p.part_lse + static_cast<size_t>(z.ctas) * 2 * fa::kKvRows;
+    p.part_o = p.part_lse + static_cast<size_t>(z.ctas) * 2 * z.rows;
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
     CUtensorMap tk, tv;
@@ -232,7 +234,10 @@ int fa_fwd_kvcache(const void* q, const void* k8, const void* v8, const float* k
     const long long rows = std::max<long long>(static_cast<long long>(num_pages) * Hk * page, page);
     if ((rc = fa::encode_cache(&tk, num_pages > 0 ? k8 : q, rows, d, page)) != FA_OK) return rc;
     if ((rc = fa::encode_cache(&tv, num_pages > 0 ? v8 : q, rows, d, page)) != FA_OK) return rc;
-    e = d == 128 ? fa::launch_few<128>(tk, tv, p, z.ctas, st) : fa::launch_few<64>(tk, tv, p, z.ctas, st);
+    if (d == 128)
+      e = z.rows == 8 ? fa::launch_few<128, 1>(tk, tv, p, z.ctas, st) : fa::launch_few<128, 2>(tk, tv, p, z.ctas, st);
+    else
+      e = z.rows == 8 ? fa::launch_few<64, 1>(tk, tv, p, z.ctas, st) : fa::launch_few<64, 2>(tk, tv, p, z.ctas, st);
     return e == cudaSuccess ? FA_OK : fa::host_cuda_fail(e);
   }
   fa::DequantParams dq{};

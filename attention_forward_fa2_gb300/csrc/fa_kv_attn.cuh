@@ -6,7 +6,7 @@
 //     o_i = sum_j softmax_j(s_j) * vs(page j) * V8_j,   lse_i = log sum_j e^{s_j}.
 // Bound by reading the codes once, 2 d bytes per key and key/value head: the
 // G = H / Hk query heads (times n_q rows) that share them are computed together,
-// 16 rows to a unit of work (sequence, key/value head, row group).
+// 8 or 16 rows to a unit of work (sequence, key/value head, row group).
 //
 // Schedule: the steps (key tiles of 128 tokens) of all units, laid end to end,
 // are cut into equal ranges, one per resident CTA, so that every SM reads the
@@ -19,9 +19,11 @@
 // TMA, a page at a time (each lane looks up and loads one page of the tile), and
 // lays out the next unit's queries; warps 0-3 compute, 32 tokens of every tile
 // each, with an online softmax of their own, and meet at the end of a unit.
-//   Products: mma.sync m16n8k16 in f16 with fp32 sums.  With 16 rows the
-//   tensor work is 1/8 of a 128-row tcgen05 tile and hides behind the loads;
-//   operands come from registers, which is where e4m3 codes become f16
+//   Products: mma.sync m16n8k16 in f16 with fp32 sums, transposed so that tokens
+//   (S^T = K Q^T) and features (O^T = V^T P^T) fill the 16 rows of a product and
+//   8 or 16 query rows its columns: with 4 heads to a key/value head, queries as
+//   rows would leave three quarters of every product empty.  The tensor work then
+//   hides behind the loads; operands come from registers, which is where e4m3 codes become f16
 //   (exact: f16 holds every e4m3 value).  q is scaled per row by a power of two
 //   to below 2^8, so that f16 holds its bf16 values exactly down to 2^-22 of the
 //   row's largest; P is rounded to f16 (2^-11, finer than bf16).
@@ -29,13 +31,13 @@
 //   multiplies the codes V8_j; the running maximum and the rescale rule work on
 //   x, so the rounding of P to f16 is relative to the largest term of the output
 //   sum, whatever the pages' scales; the normaliser adds 2^x / vs in fp32.
-//   Layout: TMA swizzles rows of d bytes; thread (n, c) = (lane / 4, lane % 4)
-//   takes 16-byte chunk c of the K row of token perm(n), whose 16 values feed four
+//   Layout: TMA swizzles rows of d bytes; thread (g, c) = (lane / 4, lane % 4)
+//   takes 16-byte chunk c of the K row of token perm(g), whose 16 values feed four
 //   k-steps (a permutation of d that q's fragments share), and V through
-//   ldmatrix.trans on byte pairs, one byte permute apart from the B fragment;
-//   perm() places the two rows that a quarter-warp reads in different banks.
-//   Occupancy: three CTAs an SM (128 registers, so q's fragments live in shared
-//   memory): a warp's step is one dependent chain of loads, products, shuffles
+//   ldmatrix.trans on byte pairs, one byte permute apart from the A fragment; P
+//   turns from S^T's layout to the B fragment by movmatrix.  perm() places the two
+//   rows that a quarter-warp reads in different banks.
+//   Occupancy: three CTAs an SM (128 registers): a warp's step is one dependent chain of loads, products, shuffles
 //   and exponentials, and other warps have to cover it.
 #pragma once
 #include <cuda.h>
@@ -49,7 +51,6 @@
 
 namespace fa {
 
-constexpr int kKvRows = 16;       // query rows per unit
 constexpr int kKvThreads = 160;   // warps 0-3 compute, warp 4 loads
 constexpr int kKvCtasPerSm = 3;
 
@@ -67,8 +68,8 @@ struct KvAttnParams {
   // an earlier CTA) or 2c + 1 (begun by c, ended later); cut[c] names the unit
   // that ends in c and was begun by an earlier CTA.
   int4* cut;                // [ctas]: b (-1: none), key/value head, first row, CTA that began it
-  float* part_o;            // [2 ctas, 16, d] normalised
-  float* part_lse;          // [2 ctas, 16], log2 units
+  float* part_o;            // [2 ctas, rows of a unit, d] normalised
+  float* part_lse;          // [2 ctas, rows of a unit], log2 units
   unsigned long long timeout_ns;
   int* status;
 };
@@ -85,17 +86,19 @@ struct KvUnit {
   int place;           // -1: whole (write o and lse), else place in the workspace
 };
 
-template <int D>
+// NT: column tiles of 8 query rows; a unit has 8 * NT.
+template <int D, int NT>
 struct KvSmem {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kTileBytes = kKvTile * D;
   static constexpr int kStageBytes = 2 * kTileBytes;               // K then V
   static constexpr int kOffConst = kStages * kStageBytes;          // per stage and page: ks, log2 vs, 1 / vs
   static constexpr int kConstBytes = 3 * (kKvTile / 16) * 4;
-  static constexpr int kOffQ = kOffConst + kStages * kConstBytes;  // two units' q as A fragments
-  static constexpr int kQBytes = (D / 16) * 32 * 16;
+  static constexpr int kOffQ = kOffConst + kStages * kConstBytes;  // two units' q as B fragments
+  static constexpr int kQBytes = NT * (D / 32) * 32 * 16;
   static constexpr int kOffCoef = kOffQ + 2 * kQBytes;             // and the factor of each row's scores
-  static constexpr int kOffUnit = kOffCoef + 2 * kKvRows * 4;
+  static constexpr int kOffUnit = kOffCoef + 2 * kRows * 4;
   static constexpr int kUnitBytes = 64;
   static constexpr int kOffBar = kOffUnit + 2 * kUnitBytes;
   static constexpr int kNumBars = 2 * kStages + 5;
@@ -104,7 +107,7 @@ struct KvSmem {
   static constexpr int kAlloc = kBytes + 1024;
   // At the end of a unit its last stage takes two warps' rows: d floats, m and l.
   static constexpr int kRowStride = D + 16;                        // floats; rows of a quarter-warp in different banks
-  static_assert(2 * kKvRows * (kRowStride + 2) * 4 <= kStageBytes, "join area");
+  static_assert(2 * kRows * (kRowStride + 2) * 4 <= kStageBytes, "join area");
   static_assert(sizeof(KvUnit) <= kUnitBytes && kOffQ % 16 == 0 && kOffBar % 8 == 0, "layout");
   static_assert(kKvCtasPerSm * (kAlloc + 1024) <= 233472, "three CTAs an SM");
 };
@@ -118,6 +121,7 @@ struct KvSeq {
   // Steps of a unit: a sequence without keys takes one, in which it sees nothing.
   __device__ __forceinline__ int steps() const { return range.steps > 0 ? range.steps : 1; }
 };
+template <int ROWS>
 __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams& p, int b) {
   KvSeq s;
   s.row0 = p.cu ? p.cu[b] : b * p.max_q;
@@ -127,7 +131,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams& p, int b) {
           s.len > static_cast<long long>(p.width) * p.page;
   if (s.bad) s.n_q = 0;
   s.rows = s.n_q * p.G;
-  s.units_per_head = (s.rows + kKvRows - 1) / kKvRows;
+  s.units_per_head = (s.rows + ROWS - 1) / ROWS;
   s.range = kv_range(p.causal ? s.len - s.n_q : s.len - 1, s.len - 1, p.window, p.sinks);
   return s;
 }
@@ -136,12 +140,13 @@ __device__ __forceinline__ long long kv_flat(const KvAttnParams& p, const KvSeq&
 }
 
 // D (16 x 8, fp32) += A (16 x 16, f16) * B (16 x 8, f16).
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
@@ -154,6 +159,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
+}
+
+// The transpose of an 8 x 8 block of 16-bit values, one row a quad.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
@@ -174,24 +186,25 @@ __device__ __forceinline__ uint32_t kv_chunk(int t, int ch) {
   return D == 128 ? t * 128 + ((ch ^ (t & 7)) << 4) : t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
 }
 
-// Token (of 8) that fragment row / column n stands for.
+// Token (of 8) that fragment row g stands for.
 template <int D>
 __device__ __forceinline__ int kv_perm(int n) {
   return D == 128 ? (n >> 1) + ((n & 1) << 2) : n;
 }
 
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
     fa_kv_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const KvAttnParams p) {
-  using L = KvSmem<D>;
-  constexpr int kSteps = D / 16;  // k-steps of S
+  using L = KvSmem<D, NT>;
+  constexpr int kRows = L::kRows;
+  constexpr int kSteps = D / 16;  // k-steps of S^T, row tiles of O^T
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw_base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = lane >> 2, c = lane & 3;
+  const int g = lane >> 2, c = lane & 3;
 
   auto full = [&](int s) -> uint32_t { return base + L::kOffBar + 8u * s; };
   auto empty = [&](int s) -> uint32_t { return base + L::kOffBar + 8u * (L::kStages + s); };
@@ -218,7 +231,7 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const KvSeq s = kv_seq(p, b);
+    const KvSeq s = kv_seq<kRows>(p, b);
     if (s.bad && blockIdx.x == 0) record_error(p.status, kErrBadSeqlens, 0);
     mine += kv_flat(p, s);
   }
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
     long long at = pre;
     int b = b0;
     for (; b < b1; ++b) {
-      const long long f = kv_flat(p, kv_seq(p, b));
+      const long long f = kv_flat(p, kv_seq<kRows>(p, b));
       if (begin < at + f) break;
       at += f;
     }
@@ -263,18 +276,18 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
     int done = 0, units = 0;
     bool ok = true;
     while (ok && pos < end) {
-      KvSeq s = kv_seq(p, b);
+      KvSeq s = kv_seq<kRows>(p, b);
       while (pos >= at + kv_flat(p, s)) {
         at += kv_flat(p, s);
-        s = kv_seq(p, ++b);
+        s = kv_seq<kRows>(p, ++b);
       }
       const int steps = s.steps();
       const long long local = pos - at;
       const int unit = static_cast<int>(local / steps), t0 = static_cast<int>(local - static_cast<long long>(unit) * steps);
       const int t1 = static_cast<int>(min(static_cast<long long>(steps), t0 + (end - pos)));
-      const int hk = unit / s.units_per_head, r0 = (unit % s.units_per_head) * kKvRows;
-      // ---- the unit and its queries, as A fragments: k-step kk = 4 h + wd takes
-      // d = 16 (c + 4 h) + 4 wd + {0, 1 | 2, 3} of rows n and n + 8.
+      const int hk = unit / s.units_per_head, r0 = (unit % s.units_per_head) * kRows;
+      // ---- the unit and its queries, as B fragments: k-step kk = 4 h + wd takes
+      // d = 16 (c + 4 h) + 4 wd + {0, 1 | 2, 3} of row 8 nt + g.
       const int us = units & 1;
       if (!ptx::mbar_wait_warp(q_empty(us), ((units >> 1) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
         if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteLoadQ);
@@ -298,11 +311,10 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
           p.cut[blockIdx.x] = make_int4(b, hk, r0, static_cast<int>((pos - t0) / span));
       }
       {
-        float* const coef = reinterpret_cast<float*>(gbase + L::kOffCoef) + us * kKvRows;
-        uint32_t frag[kSteps][4];
+        float* const coef = reinterpret_cast<float*>(gbase + L::kOffCoef) + us * kRows;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = r0 + 8 * e + n;
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = r0 + 8 * nt + g;
           const bool in = r < s.rows;
           const __nv_bfloat16* src =
               p.q + (static_cast<size_t>(s.row0 + (in ? r / p.G : 0)) * p.H + hk * p.G + (in ? r % p.G : 0)) * D;
@@ -328,22 +340,21 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
           // Exponent that brings the row's largest magnitude to [2^7, 2^8).
           const int ex = min(max(static_cast<int>(amax >> 23) - 127 - 7, -119), 119);
           const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-          if (c == 0) coef[8 * e + n] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * p.scale_log2;
+          if (c == 0) coef[8 * nt + g] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * p.scale_log2;
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
+              // Two k-steps: 16 bytes a lane.
               const uint32_t wd[4] = {raw[h][v].x, raw[h][v].y, raw[h][v].z, raw[h][v].w};
+              uint32_t f[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                frag[4 * h + 2 * v + (k >> 1)][2 * (k & 1) + e] =
-                    pack_f16x2(__uint_as_float(wd[k] << 16) * down, __uint_as_float(wd[k] & 0xffff0000u) * down);
+                f[k] = pack_f16x2(__uint_as_float(wd[k] << 16) * down, __uint_as_float(wd[k] & 0xffff0000u) * down);
+              ptx::st_shared_v4(base + L::kOffQ + us * L::kQBytes + ((nt * (D / 32) + 2 * h + v) * 32 + lane) * 16, f[0],
+                                f[1], f[2], f[3]);
             }
         }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          ptx::st_shared_v4(base + L::kOffQ + us * L::kQBytes + (k * 32 + lane) * 16, frag[k][0], frag[k][1], frag[k][2],
-                            frag[k][3]);
       }
       ptx::mbar_arrive(q_full(us));
       ++units;
@@ -425,24 +436,37 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
     const KvUnit w = *reinterpret_cast<const KvUnit*>(gbase + L::kOffUnit + us * L::kUnitBytes);
     if (w.b < 0) return;
     const uint32_t qf = base + L::kOffQ + us * L::kQBytes + lane * 16;
-    const float* const s_coef = reinterpret_cast<const float*>(gbase + L::kOffCoef) + us * kKvRows;
-    const float coef[2] = {s_coef[n], s_coef[8 + n]};
+    const float* const s_coef = reinterpret_cast<const float*>(gbase + L::kOffCoef) + us * kRows;
     const int off = w.len - w.n_q;
     const int p_min = p.causal ? off : w.len - 1, p_max = w.len - 1;
     const KvRange range = kv_range(p_min, p_max, p.window, p.sinks);
     const int lo_max = p.window > 0 ? p_max - p.window + 1 : 0;  // the last row's window starts here
-    int pos[2];  // position of rows n and n + 8; -1 for rows behind the last (nothing visible)
+    // This thread's columns of S^T and O^T: rows 8 nt + 2 c + e of the unit.
+    float coef[NT][2];
+    int pos[NT][2];  // position of the row; -1 for rows behind the last (nothing visible)
+    float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = w.r0 + 8 * e + n;
-      pos[e] = r >= w.rows ? -1 : p.causal ? r / p.G + off : w.len - 1;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = w.r0 + 8 * nt + 2 * c + e;
+        coef[nt][e] = s_coef[8 * nt + 2 * c + e];
+        pos[nt][e] = r >= w.rows ? -1 : p.causal ? r / p.G + off : w.len - 1;
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+    uint4 qr[NT == 1 ? D / 32 : 1];  // q's fragments, where the registers hold them
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) qr[k] = ld_shared_v4(qf + k * 512);
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[kSteps][2][4];  // [chunk of 16 d][even / odd d][C fragment]
+    float acc[NT][kSteps][4];  // O^T: features 16 k + 2 g (0, 1) and 16 k + 2 g + 1 (2, 3), rows 2 c and 2 c + 1
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[k][e >> 2][e & 3] = 0.f;
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][k][e] = 0.f;
 #pragma unroll 1
     for (int i = 0; i < w.steps; ++i, ++done) {
       const int s = done % L::kStages;
@@ -456,23 +480,39 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
         const uint32_t kt = base + s * L::kStageBytes + 32 * warp * D;
         const uint32_t vt = kt + L::kTileBytes;
         const float* const cst = reinterpret_cast<const float*>(gbase + L::kOffConst + s * L::kConstBytes);
-        float sc[4][4];
+        // S^T: 8-token group j = 2 mt + half is rows half * 8 + g of row tile mt.
+        float sc[NT][2][4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sc[e >> 2][e & 3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sc[nt][e >> 2][e & 3] = 0.f;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
           uint4 raw[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) raw[j] = ld_shared_v4(kt + kv_chunk<D>(8 * j + kv_perm<D>(n), c + 4 * h));
+          for (int j = 0; j < 4; ++j) raw[j] = ld_shared_v4(kt + kv_chunk<D>(8 * j + kv_perm<D>(g), c + 4 * h));
 #pragma unroll
-          for (int wd = 0; wd < 4; ++wd) {
-            const uint4 f = ld_shared_v4(qf + (4 * h + wd) * 512);
-            const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+          for (int v = 0; v < 2; ++v) {
+            uint4 qv[NT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16(wd == 0 ? raw[j].x : wd == 1 ? raw[j].y : wd == 2 ? raw[j].z : raw[j].w, b0, b1);
-              mma_f16(sc[j], a, b0, b1);
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (NT == 1)
+                qv[nt] = qr[2 * h + v];
+              else
+                qv[nt] = ld_shared_v4(qf + (nt * (D / 32) + 2 * h + v) * 512);
+            }
+#pragma unroll
+            for (int wd = 0; wd < 2; ++wd) {
+              uint32_t lo[4], hi[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                e4m3x4_to_f16(v == 0 ? (wd == 0 ? raw[j].x : raw[j].y) : (wd == 0 ? raw[j].z : raw[j].w), lo[j], hi[j]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+                  mma_f16(sc[nt][mt], lo[2 * mt], lo[2 * mt + 1], hi[2 * mt], hi[2 * mt + 1],
+                          wd == 0 ? qv[nt].x : qv[nt].z, wd == 0 ? qv[nt].y : qv[nt].w);
             }
           }
         }
@@ -485,61 +525,65 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
           const float* pc = cst + 3 * ((32 * warp + 8 * j) >> page_shift);
           const float ck = pc[0], lv = pc[1];
           inv[j] = pc[2];
-          const int ta = tok0 + 8 * j + kv_perm<D>(2 * c), tb = tok0 + 8 * j + kv_perm<D>(2 * c + 1);
+          const int tok = tok0 + 8 * j + kv_perm<D>(g);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float f = coef[e] * ck;
-            float x0 = fmaf(sc[j][2 * e], f, lv), x1 = fmaf(sc[j][2 * e + 1], f, lv);
-            if (border) {
-              const int pr = pos[e], lo = p.window > 0 ? pr - p.window + 1 : 0;
-              if (ta > pr || (ta < lo && ta >= p.sinks)) x0 = -INFINITY;
-              if (tb > pr || (tb < lo && tb >= p.sinks)) x1 = -INFINITY;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaf(sc[nt][j >> 1][2 * (j & 1) + e], coef[nt][e] * ck, lv);
+              if (border) {
+                const int pr = pos[nt][e], lo = p.window > 0 ? pr - p.window + 1 : 0;
+                if (tok > pr || (tok < lo && tok >= p.sinks)) x = -INFINITY;
+              }
+              sc[nt][j >> 1][2 * (j & 1) + e] = x;
             }
-            sc[j][2 * e] = x0;
-            sc[j][2 * e + 1] = x1;
-          }
           if (border) {
+            const int ta = tok0 + 8 * j + kv_perm<D>(2 * c), tb = tok0 + 8 * j + kv_perm<D>(2 * c + 1);
             if (!kv_needed(range, ta, 1)) vmask[j] &= 0xff00ff00u;
             if (!kv_needed(range, tb, 1)) vmask[j] &= 0x00ff00ffu;
           }
         }
         // The reference maximum moves when a row's maximum passes it by 2^8.
         bool move = false;
-        float mx[2];
+        float mx[NT][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = fmaxf(sc[0][2 * e], sc[0][2 * e + 1]);
-#pragma unroll
-          for (int j = 1; j < 4; ++j) v = ptx::fmax3(v, sc[j][2 * e], sc[j][2 * e + 1]);
-          mx[e] = v;
-          move = move || v > m[e] + 8.f;
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          float al[2];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            // The four threads of a row agree on its maximum.
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-            const bool up = mx[e] > m[e] + 8.f;
-            al[e] = up ? ptx::ex2(m[e] - mx[e]) : 1.f;  // 0 from m = -inf
-            if (up) m[e] = mx[e];
-            l[e] *= al[e];
+            mx[nt][e] = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][2 + e]), fmaxf(sc[nt][1][e], sc[nt][1][2 + e]));
+            move = move || mx[nt][e] > m[nt][e] + 8.f;
           }
+        if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k)
+          for (int nt = 0; nt < NT; ++nt) {
+            float al[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[k][e >> 2][e & 3] *= al[(e >> 1) & 1];
+            for (int e = 0; e < 2; ++e) {
+              // The eight threads of a row agree on its maximum.
+              float v = mx[nt][e];
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+              const bool up = v > m[nt][e] + 8.f;
+              al[e] = up ? ptx::ex2(m[nt][e] - v) : 1.f;  // 0 from m = -inf
+              if (up) m[nt][e] = v;
+              l[nt][e] *= al[e];
+            }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nt][k][e] *= al[e & 1];
+          }
         }
-        uint32_t pa[2][4];  // P as A fragments of two k-steps of 16 tokens
+        uint32_t pb[NT][4];  // P^T of the 8-token groups as halves of B fragments
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float neg = m[e] == -INFINITY ? 0.f : -m[e];
+        for (int nt = 0; nt < NT; ++nt) {
+          const float n0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float e0 = ptx::ex2(sc[j][2 * e] + neg), e1 = ptx::ex2(sc[j][2 * e + 1] + neg);
-            l[e] = fmaf(e0 + e1, inv[j], l[e]);
-            pa[j >> 1][2 * (j & 1) + e] = pack_f16x2(e0, e1);
+            const float e0 = ptx::ex2(sc[nt][j >> 1][2 * (j & 1)] + n0), e1 = ptx::ex2(sc[nt][j >> 1][2 * (j & 1) + 1] + n1);
+            l[nt][0] = fmaf(e0, inv[j], l[nt][0]);
+            l[nt][1] = fmaf(e1, inv[j], l[nt][1]);
+            pb[nt][j] = movmatrix_trans(pack_f16x2(e0, e1));
           }
         }
 #pragma unroll
@@ -557,11 +601,11 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
                 u0 &= vmask[2 * kk];
                 u1 &= vmask[2 * kk + 1];
               }
-              uint32_t e0, o0, e1, o1;
-              e4m3x4_to_f16(u0, e0, o0);
-              e4m3x4_to_f16(u1, e1, o1);
-              mma_f16(acc[ch + q2][0], pa[kk], e0, e1);
-              mma_f16(acc[ch + q2][1], pa[kk], o0, o1);
+              uint32_t a0, a1, a2, a3;  // even and odd features, tokens 0-7 and 8-15
+              e4m3x4_to_f16(u0, a0, a1);
+              e4m3x4_to_f16(u1, a2, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][ch + q2], a0, a1, a2, a3, pb[nt][2 * kk], pb[nt][2 * kk + 1]);
             }
           }
         }
@@ -576,43 +620,43 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
     const int last = (done - 1) % L::kStages;
     float* const area = reinterpret_cast<float*>(gbase + last * L::kStageBytes);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], k);
     auto put = [&](float* a) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float* const dst = a + (8 * e + n) * (L::kRowStride + 2);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          *reinterpret_cast<float2*>(dst + 16 * k + 4 * c) = make_float2(acc[k][0][2 * e], acc[k][1][2 * e]);
-          *reinterpret_cast<float2*>(dst + 16 * k + 4 * c + 2) = make_float2(acc[k][0][2 * e + 1], acc[k][1][2 * e + 1]);
+        for (int e = 0; e < 2; ++e) {
+          float* const dst = a + (8 * nt + 2 * c + e) * (L::kRowStride + 2);
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            *reinterpret_cast<float2*>(dst + 16 * k + 2 * g) = make_float2(acc[nt][k][e], acc[nt][k][2 + e]);
+          if (g == 0) *reinterpret_cast<float2*>(dst + L::kRowStride) = make_float2(m[nt][e], l[nt][e]);
         }
-        if (c == 0) *reinterpret_cast<float2*>(dst + L::kRowStride) = make_float2(m[e], l[e]);
-      }
     };
     auto take = [&](const float* a) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float* const src = a + (8 * e + n) * (L::kRowStride + 2);
-        const float2 ml = *reinterpret_cast<const float2*>(src + L::kRowStride);
-        const float M = fmaxf(m[e], ml.x);
-        const float f0 = M == -INFINITY ? 0.f : ptx::ex2(m[e] - M), f1 = M == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
-        m[e] = M;
-        l[e] = l[e] * f0 + ml.y * f1;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const float2 x = *reinterpret_cast<const float2*>(src + 16 * k + 4 * c);
-          const float2 y = *reinterpret_cast<const float2*>(src + 16 * k + 4 * c + 2);
-          acc[k][0][2 * e] = acc[k][0][2 * e] * f0 + x.x * f1;
-          acc[k][1][2 * e] = acc[k][1][2 * e] * f0 + x.y * f1;
-          acc[k][0][2 * e + 1] = acc[k][0][2 * e + 1] * f0 + y.x * f1;
-          acc[k][1][2 * e + 1] = acc[k][1][2 * e + 1] * f0 + y.y * f1;
+        for (int e = 0; e < 2; ++e) {
+          const float* const src = a + (8 * nt + 2 * c + e) * (L::kRowStride + 2);
+          const float2 ml = *reinterpret_cast<const float2*>(src + L::kRowStride);
+          const float M = fmaxf(m[nt][e], ml.x);
+          const float f0 = M == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - M), f1 = M == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
+          m[nt][e] = M;
+          l[nt][e] = l[nt][e] * f0 + ml.y * f1;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const float2 x = *reinterpret_cast<const float2*>(src + 16 * k + 2 * g);
+            acc[nt][k][e] = acc[nt][k][e] * f0 + x.x * f1;
+            acc[nt][k][2 + e] = acc[nt][k][2 + e] * f0 + x.y * f1;
+          }
         }
-      }
     };
-    constexpr int kArea = kKvRows * (L::kRowStride + 2);
+    constexpr int kArea = kRows * (L::kRowStride + 2);
     if (!meet()) return;  // all four have read the stage
     if (warp >= 2) put(area + (warp - 2) * kArea);
     if (!meet()) return;
@@ -622,30 +666,30 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
     if (warp == 0) {
       take(area + kArea);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = w.r0 + 8 * e + n;
-        if (r >= w.rows) continue;
-        const float il = l[e] > 0.f ? 1.f / l[e] : l[e];  // NaN stays
-        const float lse2 = l[e] > 0.f ? m[e] + log2f(l[e]) : l[e] == 0.f ? -INFINITY : l[e];
-        if (w.place >= 0) {
-          const size_t row = static_cast<size_t>(w.place) * kKvRows + 8 * e + n;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k)
-            *reinterpret_cast<float4*>(p.part_o + row * D + 16 * k + 4 * c) =
-                make_float4(acc[k][0][2 * e] * il, acc[k][1][2 * e] * il, acc[k][0][2 * e + 1] * il,
-                            acc[k][1][2 * e + 1] * il);
-          if (c == 0) p.part_lse[row] = lse2;
-        } else {
-          const int i = r / p.G, h = w.hk * p.G + r % p.G;
-          __nv_bfloat16* const dst = p.o + (static_cast<size_t>(w.row0 + i) * p.H + h) * D + 4 * c;
+        for (int e = 0; e < 2; ++e) {
+          const int r = w.r0 + 8 * nt + 2 * c + e;
+          if (r >= w.rows) continue;
+          const float lt = l[nt][e];
+          const float il = lt > 0.f ? 1.f / lt : lt;  // NaN stays
+          const float lse2 = lt > 0.f ? m[nt][e] + log2f(lt) : lt == 0.f ? -INFINITY : lt;
+          if (w.place >= 0) {
+            const size_t row = static_cast<size_t>(w.place) * kRows + 8 * nt + 2 * c + e;
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k)
-            *reinterpret_cast<uint2*>(dst + 16 * k) =
-                make_uint2(ptx::pack_bf16x2(acc[k][0][2 * e] * il, acc[k][1][2 * e] * il),
-                           ptx::pack_bf16x2(acc[k][0][2 * e + 1] * il, acc[k][1][2 * e + 1] * il));
-          if (c == 0) p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.max_q + i] = lse2 * 0.69314718055994530942f;
+            for (int k = 0; k < kSteps; ++k)
+              *reinterpret_cast<float2*>(p.part_o + row * D + 16 * k + 2 * g) =
+                  make_float2(acc[nt][k][e] * il, acc[nt][k][2 + e] * il);
+            if (g == 0) p.part_lse[row] = lse2;
+          } else {
+            const int i = r / p.G, h = w.hk * p.G + r % p.G;
+            __nv_bfloat16* const dst = p.o + (static_cast<size_t>(w.row0 + i) * p.H + h) * D + 2 * g;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+              *reinterpret_cast<uint32_t*>(dst + 16 * k) = ptx::pack_bf16x2(acc[nt][k][e] * il, acc[nt][k][2 + e] * il);
+            if (g == 0) p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.max_q + i] = lse2 * 0.69314718055994530942f;
+          }
         }
-      }
     }
     // The stage goes back to TMA: order the writes above before its copies.
     ptx::fence_proxy_async_smem();
@@ -658,7 +702,7 @@ __global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
 // it: o = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse2_s - max).  One block per row;
 // each warp adds every fourth part.  Bound by reading the parts, a few per cent of
 // the codes; a single sequence and head has one part per CTA.
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(128) fa_kv_join_kernel(const KvAttnParams p) {
   const int4 cut = p.cut[blockIdx.x];
   if (cut.x < 0) return;
@@ -670,7 +714,7 @@ __global__ void __launch_bounds__(128) fa_kv_join_kernel(const KvAttnParams p) {
   const int parts = static_cast<int>(blockIdx.x) - cut.w + 1;
   // Part s lies with CTA cut.w + s: the first is that CTA's tail, the others are heads.
   auto at = [&](int s) -> size_t {
-    return (2 * static_cast<size_t>(cut.w + s) + (s == 0 ? 1 : 0)) * kKvRows + blockIdx.y;
+    return (2 * static_cast<size_t>(cut.w + s) + (s == 0 ? 1 : 0)) * ROWS + blockIdx.y;
   };
   float M = -INFINITY;
   for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_lse[at(s)]);
