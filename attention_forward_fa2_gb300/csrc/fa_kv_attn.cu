@@ -17,9 +17,10 @@ namespace {
 
 // Query rows per key/value head (queries times heads of a group) up to which the
 // kernel for few rows runs, a unit of 8 or 16 rows at a time (the codes of later row
-// groups come from L2); above, the query chunk is long enough for 128-row tcgen05
-// tiles.
-constexpr int kFewRows = 64;
+// groups come from L2): 5.6 ns a group and 128 keys of a key/value head (64 x 8192
+// keys, 8 heads of d 128), where the bf16 copy and 128-row tiles take 54 ns, most of
+// them for the copy and for tiles that a few queries leave empty.
+constexpr int kFewRows = 128;
 
 struct KvPlan {
   bool few;
@@ -46,7 +47,7 @@ KvPlan kv_plan(int B, int max_q, int max_k, int H, int Hk, int d, int causal, in
   }
   z.rows = rows <= 8 ? 8 : 16;
   const long long all = B * static_cast<long long>(Hk) * ((rows + z.rows - 1) / z.rows) * std::max<long long>(steps, 1);
-  z.ctas = static_cast<int>(std::max<long long>(1, std::min<long long>(all, kKvCtasPerSm * num_sms)));
+  z.ctas = static_cast<int>(std::max<long long>(1, std::min<long long>(all, (z.rows == 8 || d == 64 ? 3 : kKvCtas<128, 2>) * num_sms)));
   z.ws_bytes = static_cast<size_t>(z.ctas) * (16 + 2 * z.rows * (static_cast<size_t>(d) + 1) * 4);
   return z;
 }

@@ -37,7 +37,7 @@
 //   ldmatrix.trans on byte pairs, one byte permute apart from the A fragment; P
 //   turns from S^T's layout to the B fragment by movmatrix.  perm() places the two
 //   rows that a quarter-warp reads in different banks.
-//   Occupancy: three CTAs an SM (128 registers): a warp's step is one dependent chain of loads, products, shuffles
+//   Occupancy: two or three CTAs an SM: a warp's step is one dependent chain of loads, products, shuffles
 //   and exponentials, and other warps have to cover it.
 #pragma once
 #include <cuda.h>
@@ -52,7 +52,6 @@
 namespace fa {
 
 constexpr int kKvThreads = 160;   // warps 0-3 compute, warp 4 loads
-constexpr int kKvCtasPerSm = 3;
 
 struct KvAttnParams {
   const __nv_bfloat16* q;   // [total_q, H, d], or [B, max_q, H, d] (cu null)
@@ -86,11 +85,15 @@ struct KvUnit {
   int place;           // -1: whole (write o and lse), else place in the workspace
 };
 
-// NT: column tiles of 8 query rows; a unit has 8 * NT.
+// NT: column tiles of 8 query rows; a unit has 8 * NT.  Resident CTAs of an SM: with
+// 16 rows and d = 128 the accumulators do not fit 128 registers.
+template <int D, int NT>
+constexpr int kKvCtas = D == 128 && NT > 1 ? 2 : 3;
 template <int D, int NT>
 struct KvSmem {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kCtas = kKvCtas<D, NT>;  // resident on an SM
+  static constexpr int kStages = D == 128 ? (NT > 1 ? 3 : 2) : 4;
   static constexpr int kTileBytes = kKvTile * D;
   static constexpr int kStageBytes = 2 * kTileBytes;               // K then V
   static constexpr int kOffConst = kStages * kStageBytes;          // per stage and page: ks, log2 vs, 1 / vs
@@ -109,7 +112,7 @@ struct KvSmem {
   static constexpr int kRowStride = D + 16;                        // floats; rows of a quarter-warp in different banks
   static_assert(2 * kRows * (kRowStride + 2) * 4 <= kStageBytes, "join area");
   static_assert(sizeof(KvUnit) <= kUnitBytes && kOffQ % 16 == 0 && kOffBar % 8 == 0, "layout");
-  static_assert(kKvCtasPerSm * (kAlloc + 1024) <= 233472, "three CTAs an SM");
+  static_assert(kCtas * (kAlloc + 1024) <= 233472, "resident CTAs");
 };
 
 // The queries and keys of a sequence, and the key tiles its rows see.
@@ -193,7 +196,7 @@ __device__ __forceinline__ int kv_perm(int n) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kKvThreads, kKvCtasPerSm)
+__global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
     fa_kv_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const KvAttnParams p) {
   using L = KvSmem<D, NT>;

@@ -405,7 +405,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
  *   workspace : fa_kvcache_workspace_bytes(...) bytes of device memory, 16-byte
  *             aligned, rewritten by every call (NULL when 0); calls that share one
  *             must not overlap on the GPU.  Its size depends on the current device.
- *             Long query chunks (more than 64 query rows per key/value head)
+ *             Long query chunks (more than 128 query rows per key/value head)
  *             keep a bf16 copy of the visible keys there.
  */
 int fa_kvcache_append(const void* k, const void* v, long long k_stride, long long v_stride, const void* q,
