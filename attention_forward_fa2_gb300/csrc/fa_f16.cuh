@@ -1,10 +1,17 @@
-// fa_f16.cuh -- conversions through f16 shared by the cache and window kernels.
+// fa_f16.cuh -- conversions through f16, and grid dependencies, shared by the cache and
+// window kernels.
 #pragma once
 #include <cstdint>
 
 #include "ptx.cuh"
 
 namespace fa {
+
+// Programmatic dependent launch: the first lets the next kernel of the stream, where it
+// was launched so, set up its blocks; the second, in that kernel, waits until every
+// grid before it has ended and its writes are visible.
+__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Two floats to f16 (lo in bits 0-15) and back, as a packed pair of fp32.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {

@@ -69,9 +69,10 @@ cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const KvAtt
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kKvThreads, smem, stream>>>(tk, tv, p);
+  const cudaError_t le = cudaGetLastError();
+  if (le != cudaSuccess) return le;
   const dim3 grid(ctas, std::min(8 * NT, p.max_q * p.G));
-  fa_kv_join_kernel<D, 8 * NT><<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(&fa_kv_join_kernel<D, 8 * NT>, grid, 128, stream, p);
 }
 
 // ------------------------------------------------------------- long query chunks

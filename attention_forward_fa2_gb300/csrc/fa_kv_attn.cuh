@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
   pre -= mine;  // steps before this thread's sequences
   const long long span = (total + gridDim.x - 1) / gridDim.x;
   const long long begin = blockIdx.x * span, end = min(total, begin + span);
-  if (threadIdx.x == 0 && p.cut != nullptr) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (begin >= end) return;  // the whole CTA
   if (begin >= pre && begin < pre + mine) {
     long long at = pre;
@@ -291,76 +291,80 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
       const int hk = unit / s.units_per_head, r0 = (unit % s.units_per_head) * kRows;
       // ---- the unit and its queries, as B fragments: k-step kk = 4 h + wd takes
       // d = 16 (c + 4 h) + 4 wd + {0, 1 | 2, 3} of row 8 nt + g.
-      const int us = units & 1;
-      if (!ptx::mbar_wait_warp(q_empty(us), ((units >> 1) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
-        if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteLoadQ);
-        break;
+      uint4 raw[NT][D / 64][2];  // read ahead of the first tile's copies, laid out behind them
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + 8 * nt + g;
+        const bool in = r < s.rows;
+        const __nv_bfloat16* src =
+            p.q + (static_cast<size_t>(s.row0 + (in ? r / p.G : 0)) * p.H + hk * p.G + (in ? r % p.G : 0)) * D;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            raw[nt][h][v] = in ? *reinterpret_cast<const uint4*>(src + 16 * (c + 4 * h) + 8 * v) : make_uint4(0, 0, 0, 0);
       }
-      if (lane == 0) {
-        KvUnit* const u = reinterpret_cast<KvUnit*>(gbase + L::kOffUnit + us * L::kUnitBytes);
-        u->b = b;
-        u->hk = hk;
-        u->r0 = r0;
-        u->rows = s.rows;
-        u->row0 = s.row0;
-        u->n_q = s.n_q;
-        u->len = s.len;
-        u->steps = t1 - t0;
-        u->ns = s.range.ns;
-        u->gap = s.range.gap;
-        u->t0 = t0;
-        u->place = t0 > 0 ? 2 * blockIdx.x : t1 < steps ? 2 * blockIdx.x + 1 : -1;
-        if (t0 > 0 && t1 == steps)
-          p.cut[blockIdx.x] = make_int4(b, hk, r0, static_cast<int>((pos - t0) / span));
-      }
-      {
-        float* const coef = reinterpret_cast<float*>(gbase + L::kOffCoef) + us * kRows;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int r = r0 + 8 * nt + g;
-          const bool in = r < s.rows;
-          const __nv_bfloat16* src =
-              p.q + (static_cast<size_t>(s.row0 + (in ? r / p.G : 0)) * p.H + hk * p.G + (in ? r % p.G : 0)) * D;
-          uint4 raw[D / 64][2];
-          uint32_t amax = 0;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              raw[h][v] = make_uint4(0, 0, 0, 0);
-              if (in) raw[h][v] = *reinterpret_cast<const uint4*>(src + 16 * (c + 4 * h) + 8 * v);
-            }
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const uint32_t wd[4] = {raw[h][v].x, raw[h][v].y, raw[h][v].z, raw[h][v].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) amax = max(amax, max((wd[k] << 16) & 0x7fffffffu, wd[k] & 0x7fff0000u));
-            }
-          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          // Exponent that brings the row's largest magnitude to [2^7, 2^8).
-          const int ex = min(max(static_cast<int>(amax >> 23) - 127 - 7, -119), 119);
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-          if (c == 0) coef[8 * nt + g] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * p.scale_log2;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              // Two k-steps: 16 bytes a lane.
-              const uint32_t wd[4] = {raw[h][v].x, raw[h][v].y, raw[h][v].z, raw[h][v].w};
-              uint32_t f[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                f[k] = pack_f16x2(__uint_as_float(wd[k] << 16) * down, __uint_as_float(wd[k] & 0xffff0000u) * down);
-              ptx::st_shared_v4(base + L::kOffQ + us * L::kQBytes + ((nt * (D / 32) + 2 * h + v) * 32 + lane) * 16, f[0],
-                                f[1], f[2], f[3]);
-            }
+      auto put_unit = [&]() -> bool {
+        const int us = units & 1;
+        if (!ptx::mbar_wait_warp(q_empty(us), ((units >> 1) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
+          if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteLoadQ);
+          return false;
         }
-      }
-      ptx::mbar_arrive(q_full(us));
-      ++units;
+        if (lane == 0) {
+          KvUnit* const u = reinterpret_cast<KvUnit*>(gbase + L::kOffUnit + us * L::kUnitBytes);
+          u->b = b;
+          u->hk = hk;
+          u->r0 = r0;
+          u->rows = s.rows;
+          u->row0 = s.row0;
+          u->n_q = s.n_q;
+          u->len = s.len;
+          u->steps = t1 - t0;
+          u->ns = s.range.ns;
+          u->gap = s.range.gap;
+          u->t0 = t0;
+          u->place = t0 > 0 ? 2 * blockIdx.x : t1 < steps ? 2 * blockIdx.x + 1 : -1;
+          if (t0 > 0 && t1 == steps)
+            p.cut[blockIdx.x] = make_int4(b, hk, r0, static_cast<int>((pos - t0) / span));
+        }
+        {
+          float* const coef = reinterpret_cast<float*>(gbase + L::kOffCoef) + us * kRows;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t amax = 0;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                const uint32_t wd[4] = {raw[nt][h][v].x, raw[nt][h][v].y, raw[nt][h][v].z, raw[nt][h][v].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) amax = max(amax, max((wd[k] << 16) & 0x7fffffffu, wd[k] & 0x7fff0000u));
+              }
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // Exponent that brings the row's largest magnitude to [2^7, 2^8).
+            const int ex = min(max(static_cast<int>(amax >> 23) - 127 - 7, -119), 119);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            if (c == 0) coef[8 * nt + g] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * p.scale_log2;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                // Two k-steps: 16 bytes a lane.
+                const uint32_t wd[4] = {raw[nt][h][v].x, raw[nt][h][v].y, raw[nt][h][v].z, raw[nt][h][v].w};
+                uint32_t f[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  f[k] = pack_f16x2(__uint_as_float(wd[k] << 16) * down, __uint_as_float(wd[k] & 0xffff0000u) * down);
+                ptx::st_shared_v4(base + L::kOffQ + us * L::kQBytes + ((nt * (D / 32) + 2 * h + v) * 32 + lane) * 16, f[0],
+                                  f[1], f[2], f[3]);
+              }
+          }
+        }
+        ptx::mbar_arrive(q_full(us));
+        ++units;
+        return true;
+      };
       // ---- the unit's key tiles
       auto page_of = [&](int t) -> int {  // this lane's page of step t; -1: nothing to load
         if (t >= t1 || lane >= ppt) return -1;
@@ -401,6 +405,12 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
           cst[2] = 1.f / vs;
         }
         ptx::mbar_arrive(full(st));
+        // The unit follows its first tile's copies, whose latency covers it.
+        if (t == t0 && !put_unit()) {
+          ok = false;
+          ++done;
+          break;
+        }
       }
       pos += t1 - t0;
     }
@@ -409,6 +419,7 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
       if (lane == 0) reinterpret_cast<KvUnit*>(gbase + L::kOffUnit + (units & 1) * L::kUnitBytes)->b = -1;
       ptx::mbar_arrive(q_full(units & 1));
     }
+    grid_dependents_launch();  // the join's blocks may be set up; they wait for this grid's end
     // Nothing may land in shared memory after the CTA is gone.
     for (int s = 0; s < L::kStages; ++s)
       if (done > s) ptx::mbar_wait_drain(full(s), ((done - 1 - s) / L::kStages) & 1u, p.timeout_ns);
@@ -483,132 +494,141 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
         const uint32_t kt = base + s * L::kStageBytes + 32 * warp * D;
         const uint32_t vt = kt + L::kTileBytes;
         const float* const cst = reinterpret_cast<const float*>(gbase + L::kOffConst + s * L::kConstBytes);
-        // S^T: 8-token group j = 2 mt + half is rows half * 8 + g of row tile mt.
-        float sc[NT][2][4];
+        // 32 tokens at once, or with 16 rows 16 and 16: their sums leave registers for
+        // half the scores only.
+        constexpr int MTN = NT == 1 ? 2 : 1;
+#pragma unroll 1
+        for (int t8 = 0; t8 < 32; t8 += 16 * MTN) {
+          // S^T: 8-token group j = 2 mt + half is rows half * 8 + g of row tile mt.
+          float sc[NT][MTN][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sc[nt][e >> 2][e & 3] = 0.f;
+            for (int e = 0; e < 4 * MTN; ++e) sc[nt][e >> 2][e & 3] = 0.f;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          uint4 raw[4];
+          for (int h = 0; h < D / 64; ++h) {
+            uint4 raw[2 * MTN];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) raw[j] = ld_shared_v4(kt + kv_chunk<D>(8 * j + kv_perm<D>(g), c + 4 * h));
+            for (int j = 0; j < 2 * MTN; ++j) raw[j] = ld_shared_v4(kt + kv_chunk<D>(t8 + 8 * j + kv_perm<D>(g), c + 4 * h));
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint4 qv[NT];
+            for (int v = 0; v < 2; ++v) {
+              uint4 qv[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (NT == 1)
-                qv[nt] = qr[2 * h + v];
-              else
-                qv[nt] = ld_shared_v4(qf + (nt * (D / 32) + 2 * h + v) * 512);
-            }
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (NT == 1)
+                  qv[nt] = qr[2 * h + v];
+                else
+                  qv[nt] = ld_shared_v4(qf + (nt * (D / 32) + 2 * h + v) * 512);
+              }
 #pragma unroll
-            for (int wd = 0; wd < 2; ++wd) {
-              uint32_t lo[4], hi[4];
+              for (int wd = 0; wd < 2; ++wd) {
+                uint32_t lo[2 * MTN], hi[2 * MTN];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                e4m3x4_to_f16(v == 0 ? (wd == 0 ? raw[j].x : raw[j].y) : (wd == 0 ? raw[j].z : raw[j].w), lo[j], hi[j]);
+                for (int j = 0; j < 2 * MTN; ++j)
+                  e4m3x4_to_f16(v == 0 ? (wd == 0 ? raw[j].x : raw[j].y) : (wd == 0 ? raw[j].z : raw[j].w), lo[j], hi[j]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-                  mma_f16(sc[nt][mt], lo[2 * mt], lo[2 * mt + 1], hi[2 * mt], hi[2 * mt + 1],
-                          wd == 0 ? qv[nt].x : qv[nt].z, wd == 0 ? qv[nt].y : qv[nt].w);
+                  for (int mt = 0; mt < MTN; ++mt)
+                    mma_f16(sc[nt][mt], lo[2 * mt], lo[2 * mt + 1], hi[2 * mt], hi[2 * mt + 1],
+                            wd == 0 ? qv[nt].x : qv[nt].z, wd == 0 ? qv[nt].y : qv[nt].w);
+              }
             }
           }
-        }
-        // Exponents x, masked where a border runs through these 32 tokens.
-        const bool border = tok0 + 31 > p_min || (tok0 < lo_max && tok0 + 31 >= p.sinks);
-        float inv[4];
-        uint32_t vmask[4] = {~0u, ~0u, ~0u, ~0u};  // bytes of V fragments whose token no row sees
+          // Exponents x, masked where a border runs through these tokens.
+          const int tk = tok0 + t8;
+          const bool border = tk + 16 * MTN - 1 > p_min || (tk < lo_max && tk + 16 * MTN - 1 >= p.sinks);
+          float inv[2 * MTN];
+          uint32_t vmask[2 * MTN];  // bytes of V fragments whose token some row sees
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float* pc = cst + 3 * ((32 * warp + 8 * j) >> page_shift);
-          const float ck = pc[0], lv = pc[1];
-          inv[j] = pc[2];
-          const int tok = tok0 + 8 * j + kv_perm<D>(g);
+          for (int j = 0; j < 2 * MTN; ++j) {
+            vmask[j] = ~0u;
+            const float* pc = cst + 3 * ((32 * warp + t8 + 8 * j) >> page_shift);
+            const float ck = pc[0], lv = pc[1];
+            inv[j] = pc[2];
+            const int tok = tk + 8 * j + kv_perm<D>(g);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = fmaf(sc[nt][j >> 1][2 * (j & 1) + e], coef[nt][e] * ck, lv);
+                if (border) {
+                  const int pr = pos[nt][e], lo = p.window > 0 ? pr - p.window + 1 : 0;
+                  if (tok > pr || (tok < lo && tok >= p.sinks)) x = -INFINITY;
+                }
+                sc[nt][j >> 1][2 * (j & 1) + e] = x;
+              }
+            if (border) {
+              const int ta = tk + 8 * j + kv_perm<D>(2 * c), tb = tk + 8 * j + kv_perm<D>(2 * c + 1);
+              if (!kv_needed(range, ta, 1)) vmask[j] &= 0xff00ff00u;
+              if (!kv_needed(range, tb, 1)) vmask[j] &= 0x00ff00ffu;
+            }
+          }
+          // The reference maximum moves when a row's maximum passes it by 2^8.
+          bool move = false;
+          float mx[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = fmaf(sc[nt][j >> 1][2 * (j & 1) + e], coef[nt][e] * ck, lv);
-              if (border) {
-                const int pr = pos[nt][e], lo = p.window > 0 ? pr - p.window + 1 : 0;
-                if (tok > pr || (tok < lo && tok >= p.sinks)) x = -INFINITY;
-              }
-              sc[nt][j >> 1][2 * (j & 1) + e] = x;
+              mx[nt][e] = fmaxf(sc[nt][0][e], sc[nt][0][2 + e]);
+              if constexpr (MTN == 2) mx[nt][e] = fmaxf(mx[nt][e], fmaxf(sc[nt][MTN - 1][e], sc[nt][MTN - 1][2 + e]));
+              move = move || mx[nt][e] > m[nt][e] + 8.f;
             }
-          if (border) {
-            const int ta = tok0 + 8 * j + kv_perm<D>(2 * c), tb = tok0 + 8 * j + kv_perm<D>(2 * c + 1);
-            if (!kv_needed(range, ta, 1)) vmask[j] &= 0xff00ff00u;
-            if (!kv_needed(range, tb, 1)) vmask[j] &= 0x00ff00ffu;
-          }
-        }
-        // The reference maximum moves when a row's maximum passes it by 2^8.
-        bool move = false;
-        float mx[NT][2];
+          if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+              float al[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mx[nt][e] = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][2 + e]), fmaxf(sc[nt][1][e], sc[nt][1][2 + e]));
-            move = move || mx[nt][e] > m[nt][e] + 8.f;
+              for (int e = 0; e < 2; ++e) {
+                // The eight threads of a row agree on its maximum.
+                float v = mx[nt][e];
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+                const bool up = v > m[nt][e] + 8.f;
+                al[e] = up ? ptx::ex2(m[nt][e] - v) : 1.f;  // 0 from m = -inf
+                if (up) m[nt][e] = v;
+                l[nt][e] *= al[e];
+              }
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][k][e] *= al[e & 1];
+            }
           }
-        if (__any_sync(0xffffffffu, move)) {
+          uint32_t pb[NT][2 * MTN];  // P^T of the 8-token groups as halves of B fragments
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float al[2];
+            const float n0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              // The eight threads of a row agree on its maximum.
-              float v = mx[nt][e];
-#pragma unroll
-              for (int k = 4; k < 32; k <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
-              const bool up = v > m[nt][e] + 8.f;
-              al[e] = up ? ptx::ex2(m[nt][e] - v) : 1.f;  // 0 from m = -inf
-              if (up) m[nt][e] = v;
-              l[nt][e] *= al[e];
+            for (int j = 0; j < 2 * MTN; ++j) {
+              const float e0 = ptx::ex2(sc[nt][j >> 1][2 * (j & 1)] + n0), e1 = ptx::ex2(sc[nt][j >> 1][2 * (j & 1) + 1] + n1);
+              l[nt][0] = fmaf(e0, inv[j], l[nt][0]);
+              l[nt][1] = fmaf(e1, inv[j], l[nt][1]);
+              pb[nt][j] = movmatrix_trans(pack_f16x2(e0, e1));
             }
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][k][e] *= al[e & 1];
           }
-        }
-        uint32_t pb[NT][4];  // P^T of the 8-token groups as halves of B fragments
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float n0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
+          for (int kk = 0; kk < MTN; ++kk) {
+            // Matrix lane / 8: tokens 8 (bit 0) of the 16, chunk (bit 1) of the pair.
+            const int trow = t8 + 16 * kk + ((lane >> 3) & 1) * 8 + kv_perm<D>(lane & 7);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float e0 = ptx::ex2(sc[nt][j >> 1][2 * (j & 1)] + n0), e1 = ptx::ex2(sc[nt][j >> 1][2 * (j & 1) + 1] + n1);
-            l[nt][0] = fmaf(e0, inv[j], l[nt][0]);
-            l[nt][1] = fmaf(e1, inv[j], l[nt][1]);
-            pb[nt][j] = movmatrix_trans(pack_f16x2(e0, e1));
-          }
-        }
+            for (int ch = 0; ch < kSteps; ch += 2) {
+              uint32_t r[4];
+              ldmatrix_x4_trans(vt + kv_chunk<D>(trow, ch + (lane >> 4)), r);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          // Matrix lane / 8: tokens 8 (bit 0) of the 16, chunk (bit 1) of the pair.
-          const int trow = 16 * kk + ((lane >> 3) & 1) * 8 + kv_perm<D>(lane & 7);
+              for (int q2 = 0; q2 < 2; ++q2) {
+                uint32_t u0 = __byte_perm(r[2 * q2], 0, 0x3120), u1 = __byte_perm(r[2 * q2 + 1], 0, 0x3120);
+                if (border) {
+                  u0 &= vmask[2 * kk];
+                  u1 &= vmask[2 * kk + 1];
+                }
+                uint32_t a0, a1, a2, a3;  // even and odd features, tokens 0-7 and 8-15
+                e4m3x4_to_f16(u0, a0, a1);
+                e4m3x4_to_f16(u1, a2, a3);
 #pragma unroll
-          for (int ch = 0; ch < kSteps; ch += 2) {
-            uint32_t r[4];
-            ldmatrix_x4_trans(vt + kv_chunk<D>(trow, ch + (lane >> 4)), r);
-#pragma unroll
-            for (int q2 = 0; q2 < 2; ++q2) {
-              uint32_t u0 = __byte_perm(r[2 * q2], 0, 0x3120), u1 = __byte_perm(r[2 * q2 + 1], 0, 0x3120);
-              if (border) {
-                u0 &= vmask[2 * kk];
-                u1 &= vmask[2 * kk + 1];
+                for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][ch + q2], a0, a1, a2, a3, pb[nt][2 * kk], pb[nt][2 * kk + 1]);
               }
-              uint32_t a0, a1, a2, a3;  // even and odd features, tokens 0-7 and 8-15
-              e4m3x4_to_f16(u0, a0, a1);
-              e4m3x4_to_f16(u1, a2, a3);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][ch + q2], a0, a1, a2, a3, pb[nt][2 * kk], pb[nt][2 * kk + 1]);
             }
           }
         }
@@ -707,6 +727,7 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
 // the codes; a single sequence and head has one part per CTA.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) fa_kv_join_kernel(const KvAttnParams p) {
+  grid_dependency_wait();
   const int4 cut = p.cut[blockIdx.x];
   if (cut.x < 0) return;
   const int r = cut.z + blockIdx.y;

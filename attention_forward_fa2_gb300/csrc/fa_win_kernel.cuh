@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "fa_f16.cuh"
 #include "fa_fwd_kernel.cuh"
 #include "ptx.cuh"
 
@@ -493,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           cur.u += gridDim.x;
         }
       }
+      if constexpr (KPAD) grid_dependents_launch();  // the join's blocks may be set up; they wait for this grid's end
       // Nothing may land in shared memory after the CTA is gone.
       if (clc_pending) ptx::mbar_wait_drain(bar(L::kBarClc), n_clc & 1u, tmo);
       if (qcount > 0) ptx::mbar_wait_drain(bar(L::kBarQFull), (qcount - 1) & 1u, tmo);
@@ -885,33 +887,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The parts of the unit that ends in CTA blockIdx.x's range and was begun before
 // it ("GPU 内核与 FlashAttention" §11.2): o = sum_s w_s O_s / sum_s w_s with w_s =
-// e^(LSE_s - max).  One warp per row; bound by reading the parts.
+// e^(LSE_s - max).  One warp per row; bound by reading the parts (twice 256 rows a
+// CTA at most).
 template <int D, bool VARLEN>
 __global__ void __launch_bounds__(256) fa_win_join_kernel(const WinParams p) {
+  grid_dependency_wait();
   const int2 cut = p.cut[blockIdx.x];
   if (cut.x < 0) return;
   const WinUnit w = win_decode<128, VARLEN, true>(p, cut.x);
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (w.q_row0 + r >= w.q_end) return;
   const int parts = static_cast<int>(blockIdx.x) - cut.y + 1;
+  constexpr int kPer = D / 32;
   auto at = [&](int s) -> size_t { return (2 * static_cast<size_t>(cut.y + s) + (s == 0 ? 1 : 0)) * (kBR * kQT) + r; };
   float M = -INFINITY;
   for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_lse[at(s)]);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-  constexpr int kPer = D / 32;
   float acc[kPer], l = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int s = 0; s < parts; ++s) {
     const float ls = p.part_lse[at(s)];
-    if (ls == -INFINITY) continue;  // a part without keys holds no values
-    const float f = ptx::ex2((ls - M) * 1.44269504088896340736f);
+    const bool none = ls == -INFINITY;  // a part without keys holds no values
+    const float f = none ? 0.f : ptx::ex2((ls - M) * 1.44269504088896340736f);
     const float* src = p.part_o + at(s) * D + lane * kPer;
     l += f;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+    for (int e = 0; e < kPer; ++e) {
+      const float x = src[e];
+      acc[e] = none ? acc[e] : fmaf(f, x, acc[e]);
+    }
   }
   const float il = l > 0.f ? 1.f / l : l;
   const size_t row = VARLEN ? static_cast<size_t>(w.q_row0 + r) : static_cast<size_t>(w.b) * p.Nq + w.q_row0 + r;
