@@ -72,7 +72,7 @@ cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const KvAtt
   const cudaError_t le = cudaGetLastError();
   if (le != cudaSuccess) return le;
   const dim3 grid(ctas, std::min(8 * NT, p.max_q * p.G));
-  return launch_dependent(&fa_kv_join_kernel<D, 8 * NT>, grid, 128, stream, p);
+  return launch_dependent(&fa_kv_join_kernel<D, 8 * NT>, grid, 128, 0, stream, p);
 }
 
 // ------------------------------------------------------------- long query chunks
@@ -91,6 +91,7 @@ struct DequantParams {
 
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv_dequant_kernel(const DequantParams p) {
+  grid_dependents_launch();  // the window kernel may be set up; it waits for this grid's end
   const int b = blockIdx.y;
   const int t0 = blockIdx.x * 64;
   const bool is_k = blockIdx.z == 0;

@@ -219,11 +219,14 @@ struct WinSmem {
   static_assert(kAlloc <= 232448, "shared memory budget exceeded");
 };
 
-// KPAD: steps of unit (b, query block mb) of any head, at least one where it has rows.
+// KPAD: steps of unit (b, query block mb) of any head, at least one where it has rows,
+// behind kUnitCost more that stand for what its beginning and end take (with them
+// left out, SMs with three or four short units ended 20 % behind those with one).
+constexpr int kUnitCost = 2;
 template <bool VARLEN>
 __device__ __forceinline__ int win_flat(const WinParams& p, int b, int mb) {
   const WinUnit w = win_decode<128, VARLEN, true>(p, b * p.H * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - mb : mb));
-  return w.rows[0] ? max(w.nsteps, 1) : 0;
+  return w.rows[0] ? kUnitCost + max(w.nsteps, 1) : 0;
 }
 
 #define FA_WIN_FOR_EACH_ITEM(it) \
@@ -402,25 +405,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       auto range_item = [&]() -> WinItem {
-        if (pos >= end) return WinItem{-1, 0, 0, -1};
-        while (pos >= kat + static_cast<long long>(kw) * p.H) {
-          kat += static_cast<long long>(kw) * p.H;
-          if (++kmb == p.num_mblocks) {
-            kmb = 0;
-            ++kb;
+        while (pos < end) {
+          while (pos >= kat + static_cast<long long>(kw) * p.H) {
+            kat += static_cast<long long>(kw) * p.H;
+            if (++kmb == p.num_mblocks) {
+              kmb = 0;
+              ++kb;
+            }
+            kw = win_flat<VARLEN>(p, kb, kmb);
           }
-          kw = win_flat<VARLEN>(p, kb, kmb);
+          const int h = static_cast<int>((pos - kat) / kw), at = static_cast<int>((pos - kat) % kw);
+          const int to = static_cast<int>(min(static_cast<long long>(kw), at + (end - pos)));
+          const long long step0 = pos - at + kUnitCost;  // where the unit's steps begin
+          pos += to - at;
+          const int j0 = max(at - kUnitCost, 0), j1 = to - kUnitCost;
+          if (j1 <= j0) continue;  // the range ends ahead of the unit's first step
+          const int u = (kb * p.H + h) * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - kmb : kmb);
+          const int c = static_cast<int>(blockIdx.x);
+          if (j0 > 0 && to == kw) p.cut[c] = make_int2(u, static_cast<int>(step0 / span));
+          return WinItem{u, j0, j1, j0 > 0 ? 2 * c : to < kw ? 2 * c + 1 : -1};
         }
-        const int h = static_cast<int>((pos - kat) / kw), j0 = static_cast<int>((pos - kat) % kw);
-        const int j1 = static_cast<int>(min(static_cast<long long>(kw), j0 + (end - pos)));
-        const int u = (kb * p.H + h) * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - kmb : kmb);
-        const int place = j0 > 0 ? 2 * static_cast<int>(blockIdx.x) : j1 < kw ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
-        if (j0 > 0 && j1 == kw) p.cut[blockIdx.x] = make_int2(u, static_cast<int>((pos - j0) / span));
-        pos += j1 - j0;
-        return WinItem{u, j0, j1, place};
+        return WinItem{-1, 0, 0, -1};
       };
       WinItem cur{static_cast<int>(blockIdx.x), 0, 0, -1};
-      if constexpr (KPAD) cur = range_item();
+      if constexpr (KPAD) {
+        cur = range_item();
+        grid_dependency_wait();  // the copy of the keys is made by the kernel before this one
+      }
       if constexpr (kRing) ok = publish(cur);
       if constexpr (VARLEN && !KPAD) {
         if (ok) request();

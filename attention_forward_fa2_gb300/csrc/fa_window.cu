@@ -26,13 +26,13 @@ cudaError_t launch_win(const WinLaunchArgs& a) {
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   const int grid = KPAD ? a.num_sms : VARLEN ? a.p.num_units : std::min(a.p.num_units, a.num_sms);
-  kern<<<grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
   if constexpr (KPAD) {
-    const cudaError_t le = cudaGetLastError();
+    const cudaError_t le = launch_dependent(kern, dim3(grid), kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
     if (le != cudaSuccess) return le;
     const dim3 rows(grid, (std::min(a.p.Nq, kBR * kQT) + 7) / 8);
-    return launch_dependent(&fa_win_join_kernel<D, VARLEN>, rows, 256, a.stream, a.p);
+    return launch_dependent(&fa_win_join_kernel<D, VARLEN>, rows, 256, 0, a.stream, a.p);
   }
+  kern<<<grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
   return cudaGetLastError();
 }
 

@@ -9,18 +9,19 @@ namespace fa {
 
 // Launches a kernel that begins with grid_dependency_wait() behind the one before it on
 // the stream: its blocks are set up while that one still runs.
-template <typename P>
-cudaError_t launch_dependent(void (*kern)(P), dim3 grid, int threads, cudaStream_t stream, const P& p) {
+template <typename... P>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const P&... p) {
   cudaLaunchConfig_t c = {};
   c.gridDim = grid;
   c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
   c.stream = stream;
   cudaLaunchAttribute a;
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &a;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, p);
+  return cudaLaunchKernelEx(&c, kern, p...);
 }
 
 struct WinLaunchArgs {
