@@ -89,6 +89,7 @@ struct WinParams {
   int window, sinks;
   int full;                    // 1: no causal border
   int by_block;                // 1: units numbered query block by query block
+  int whole;                   // KPAD: units are not cut (see WinItem)
   int num_mblocks;             // ceil(Nq / (kBR * kQT))
   int num_units;               // B * H * num_mblocks
   int total_q, total_k;        // variable-length form: packed rows (sequences past them are rejected)
@@ -202,8 +203,10 @@ __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
 //   KPAD (few queries, many keys): the steps of all units, laid end to end, are cut
 //     into one range per SM; the load thread hands units, and the parts of units
 //     cut by the range's borders, through the ring; fa_win_join_kernel joins the
-//     parts.  Three prompts of at most 1024 queries over 8192 keys, 16 heads: 92 us
-//     of whole units left most SMs idle behind the longest (195 us).
+//     parts.  (Three prompts of at most 1024 queries over 8192 keys, 16 heads: as
+//     whole units 195 us, most SMs idle behind the longest; cut 102.)  With many
+//     units an SM (`whole`) they are handed out whole, as packed ones are, which
+//     keeps the units in flight on the keys of a few heads in L2.
 struct WinItem {
   int u, j0, j1, place;  // u < 0: no more
 };
@@ -233,7 +236,9 @@ __device__ __forceinline__ int win_flat(const WinParams& p, int b, int mb) {
   for (WinItem it = next_item(-1); it.u >= 0 && it.u < p.num_units && ok; it = next_item(it.u))
 #define FA_WIN_UNIT(it)                                       \
   WinUnit w = win_decode<BC, VARLEN, KPAD>(p, (it).u);        \
-  if constexpr (KPAD) win_restrict(w, (it).j0, (it).j1, (it).place)
+  if constexpr (KPAD) {                                       \
+    if (!p.whole) win_restrict(w, (it).j0, (it).j1, (it).place); \
+  }
 
 template <int D, int STAGES, bool VARLEN, bool KPAD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // sequence, query blocks in order, heads innermost), from a scan of the lengths.
   long long begin = 0, end = 0, span = 1;
   long long* const s_scan = reinterpret_cast<long long*>(gbase + WinSmem<D, STAGES>::kOffScan);
-  if constexpr (KPAD) {
+  if (KPAD && !p.whole) {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     auto flat = [&](int b) -> long long {
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // KPAD: where the range stands: sequence, its first step, query block, its first step.
       int kb = 0, kmb = 0, kw = 0;
       long long kat = 0, pos = begin;
-      if constexpr (KPAD) {
+      if (KPAD && !p.whole) {
         if (begin < end) {
           kb = static_cast<int>(s_scan[kThreads / 32]);
           kat = s_scan[kThreads / 32 + 1];
@@ -428,17 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         return WinItem{-1, 0, 0, -1};
       };
       WinItem cur{static_cast<int>(blockIdx.x), 0, 0, -1};
-      if constexpr (KPAD) {
-        cur = range_item();
-        grid_dependency_wait();  // the copy of the keys is made by the kernel before this one
-      }
+      const bool ranges = KPAD && !p.whole;
+      if (ranges) cur = range_item();
+      if constexpr (KPAD) grid_dependency_wait();  // the copy of the keys is made by the kernel before this one
       if constexpr (kRing) ok = publish(cur);
-      if constexpr (VARLEN && !KPAD) {
-        if (ok) request();
-      }
+      if (kRing && !ranges && ok) request();
 #pragma unroll 1
       while (ok && cur.u >= 0 && cur.u < p.num_units) {
-        FA_WIN_UNIT(cur);
+        FA_WIN_UNIT(cur)
         if (w.run) {
           if (!ptx::mbar_wait(bar(L::kBarQEmpty), (qcount & 1u) ^ 1u, s_abort, tmo)) {
             record_error(p.status, kErrTimeout, kSiteLoadQ);
@@ -488,10 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        if constexpr (KPAD) {
+        if (ranges) {
           cur = range_item();
           if (!publish(cur)) break;
-        } else if constexpr (VARLEN) {
+        } else if constexpr (kRing) {
           if (!ptx::mbar_wait(bar(L::kBarClc), n_clc & 1u, s_abort, tmo)) {
             record_error(p.status, kErrTimeout, kSiteItem);
             break;
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 #pragma unroll 1
       FA_WIN_FOR_EACH_ITEM(it) {
-        FA_WIN_UNIT(it);
+        FA_WIN_UNIT(it)
         if (!w.run) continue;
         if (!wait(bar(L::kBarQFull), qcount & 1u, kSiteMmaQ)) break;
         ++qcount;
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     FA_WIN_FOR_EACH_ITEM(it) {
-      FA_WIN_UNIT(it);
+      FA_WIN_UNIT(it)
       const RowWindow qw = t == 0 ? w.qwin[0] : w.qwin[1];
       // Place of this row's partial results (row of the unit).
       const size_t part = KPAD && w.place >= 0
@@ -795,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 #pragma unroll 1
     FA_WIN_FOR_EACH_ITEM(it) {
-      FA_WIN_UNIT(it);
+      FA_WIN_UNIT(it)
       if (w.nokeys) {
         zero_rows(w, w.q_row0, min(kBR * kQT, w.q_end - w.q_row0));
         continue;

@@ -25,16 +25,21 @@ cudaError_t launch_win(const WinLaunchArgs& a) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
-  const int grid = KPAD ? a.num_sms : VARLEN ? a.p.num_units : std::min(a.p.num_units, a.num_sms);
+  const int grid = KPAD && !a.p.whole ? a.num_sms
+                   : KPAD || VARLEN   ? a.p.num_units
+                                      : std::min(a.p.num_units, a.num_sms);
   if constexpr (KPAD) {
     const cudaError_t le = launch_dependent(kern, dim3(grid), kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
-    if (le != cudaSuccess) return le;
+    if (le != cudaSuccess || a.p.whole) return le;
     const dim3 rows(grid, (std::min(a.p.Nq, kBR * kQT) + 7) / 8);
     return launch_dependent(&fa_win_join_kernel<D, VARLEN>, rows, 256, 0, a.stream, a.p);
   }
   kern<<<grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
   return cudaGetLastError();
 }
+
+// KPAD: units an SM from which they are handed out whole (WinItem in fa_win_kernel.cuh).
+constexpr long long kWholeUnits = 6;
 
 template <int D>
 cudaError_t dispatch_win(const WinLaunchArgs& a, bool varlen, bool kpad) {
@@ -143,6 +148,7 @@ int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v,
   // the kernel's index arithmetic stays in 32 bits.
   p.window = std::min(p.window, std::max(p.Nk, 1));
   p.sinks = std::min(p.sinks, p.Nk);
+  p.whole = kpad && units >= kWholeUnits * a.num_sms;
   p.by_block = !varlen && !kpad && p.window >= p.Nk / 2;
   p.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
   // A row's first tile may show it a single key (the window's start, few sinks),

@@ -336,6 +336,13 @@ def test_long_query_chunks(d, causal):
     _attend_and_check([600, 900, 300, 2, 0], 300, 8, 2, d, 64, causal=causal)
 
 
+@pytest.mark.parametrize("packed", [None, [260, 1, 0, 200, 300, 77, 260, 129] * 2])
+def test_long_chunks_of_many_heads(packed):
+    """More than six units an SM: they are handed out whole instead of cut into ranges."""
+    _attend_and_check([300, 500, 260, 411] * 4 if packed is None else [300, 500, 10, 411] * 4, 260, 32, 2, 64, 32,
+                      packed=packed, window=0 if packed is None else 150, sinks=0 if packed is None else 3)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("packed", [[1, 3, 0, 2], [129, 0, 1, 300]])
 def test_packed_queries(d, packed):
@@ -350,6 +357,83 @@ def test_page_scales_that_differ_widely():
 def test_many_splits_and_loose_bound():
     _attend_and_check([9000], 1, 4, 1, 128, 64)
     _attend_and_check([90, 9000], 1, 4, 1, 64, 128, max_k=40_000)
+
+
+def test_rows_behind_the_last_sequence_are_left():
+    c, table = _full_cache([40, 300], 2, 16, 64, 5)
+    for new in ([3, 2], [150, 200]):
+        T = sum(new) + 4
+        q, cu = _rand((T, 4, 64), 1), _ints([0, new[0], sum(new)])
+        out = torch.full_like(q, 7.0)
+        fa.forward_kvcache(q, c, table, _ints([40, 300]), 300, cu_seqlens_q=cu, max_seqlen_q=max(new), out=out)
+        _status()
+        assert (out[-4:] == 7.0).all() and not (out[:-4] == 7.0).all(-1).any()
+    k = _rand((9, 2, 64), 2)
+    out = torch.full((9, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    before = c.k8.clone()
+    fa.append_kvcache(c, k, k, table, _ints([30, 200]), q=_rand((9, 4, 64), 3), q_out=out, cu_seqlens=_ints([0, 2, 5]),
+                      max_seqlen=3)
+    _status()
+    assert (out[5:] == 7.0).all() and not (out[:5] == 7.0).all(-1).any()
+    assert int((before != c.k8).any(-1).sum()) <= 2 * 5 + 2 * 2 * 15  # new slots, and older ones of the two pages
+
+
+def test_offsets_past_32_bits():
+    """Pages that begin past 2^32 bytes of codes, in every path."""
+    Hk, page, d = 8, 128, 128
+    pages = (1 << 32) // (Hk * page * d) + 40
+    c = fa.KvCache.empty(pages, page, Hk, d)
+    lens = [300, 129]
+    table = _ints([[pages - 1, pages - 3, pages - 8], [pages - 2, pages - 5, 0]])
+    x = _rand((sum(lens), 4 * Hk + 2 * Hk, d), 1)
+    cu = _ints([0, 300, 429])
+    fa.append_kvcache(c, x[:, 32:40], x[:, 40:], table, _ints([0, 0]), cu_seqlens=cu, max_seqlen=300)
+    _status()
+    for b in range(2):
+        k, v = _values(c, table, b, lens[b])
+        rows = x[int(cu[b]):int(cu[b + 1])].double()
+        for got, want in ((k, rows[:, 32:40]), (v, rows[:, 40:])):
+            assert ((got - want).abs() <= want.abs() * (2.0 ** -4 + 2.0 ** -20) + 2.0 ** -10 * 2.0 ** -6).all()
+    for n in (1, 60):
+        q = _rand((2, n, 32, d), 2)
+        o, lse = fa.forward_kvcache(q, c, table, _ints(lens), 300)
+        _status()
+        for b in range(2):
+            k, v = _values(c, table, b, lens[b])
+            ref, lref, bound = _reference(q[b], k, v, 2.0 ** -6, d ** -0.5, R.visible(n, lens[b], 0, 0, device="cuda"), n == 1)
+            R.check(o[b], ref, bound, "o")
+            R.check_lse(lse[b], lref, "lse")
+
+
+def test_on_another_stream():
+    """The calls run on the stream they are given, and what they allocate belongs to it."""
+    c, table = _full_cache([900], 2, 32, 128, 6)
+    q, lens = _rand((1, 1, 8, 128), 1), _ints([900])
+    o, lse = fa.forward_kvcache(q, c, table, lens, 900)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, lse2 = fa.forward_kvcache(q, c, table, lens, 900, stream=side)
+    k = _rand((1, 1, 2, 128), 2)
+    qr = fa.append_kvcache(c, k, k, table, _ints([100]), q=q, stream=side)
+    side.synchronize()
+    _status()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(qr, q)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with a workspace of its own: the same bits as one after the other."""
+    c, table = _full_cache([3000, 1700], 4, 64, 128, 7)
+    lens = _ints([3000, 1700])
+    qs = [_rand((2, n, 16, 128), n) for n in (1, 40)]
+    one = [fa.forward_kvcache(q, c, table, lens, 3000) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        two = [fa.forward_kvcache(q, c, table, lens, 3000, stream=s) for q, s in zip(qs, streams)]
+        torch.cuda.synchronize()
+        for (a, b), (x, y) in zip(one, two):
+            assert torch.equal(a, x) and torch.equal(b, y)
+    _status()
 
 
 def test_outliers_in_queries_keep_their_row():
@@ -408,6 +492,9 @@ def test_refusals():
         fa.append_kvcache(c, k, k, table, lens, cos=torch.zeros(9, 32, device="cuda"))
     with pytest.raises(fa.FaError):
         fa.append_kvcache(c, k, k, table, lens, cos=torch.zeros(9, 12, device="cuda"), sin=torch.zeros(9, 12, device="cuda"))
+    with pytest.raises(fa.FaError):  # rows that do not begin on 16 bytes
+        x = _rand((1, 4, 129 * 2 + 4,), 3)[..., 4:260].unflatten(-1, (4, 64))
+        fa.append_kvcache(c, x[:, :, :2], x[:, :, 2:], table, lens)
     with pytest.raises(fa.FaError):  # the same row for every token
         x = _rand((1, 1, 2, 64), 3).expand(1, 4, 2, 64)
         fa.append_kvcache(c, x, x, table, lens)
