@@ -18,9 +18,12 @@
 //     kt(j) = j            for j < ns     (tiles that hold sinks, below the windows)
 //     kt(j) = j + gap      for j >= ns    (from the first tile of tile 0's window
 //                                          to the diagonal of tile 1)
-// and query tile t takes part in step j only when it sees a key of kt(j): tile
-// 1's window starts and ends one key tile after tile 0's, so each tile runs its
-// own products, and nothing runs for tiles between the sinks and the window.
+// and query tile t takes part in step j only when it sees a key of kt(j).  Where two
+// query heads share their keys, the tiles of a unit are the same rows of two heads
+// (`pair`): both see the same key tiles, and every step runs both.  Else they are
+// 256 rows of one head; tile 1's window starts and ends one key tile after tile 0's,
+// so each runs its own products.  Nothing runs for tiles between the sinks and the
+// window.
 // The work of a unit is thus bound by the window, whatever the length; what is
 // lost is the masked part of the first and last key tile of the window and of
 // the sink tile (window 1024, 64 sinks: 10 products of 128 x 128 for 8.5 x 128
@@ -65,6 +68,7 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : (
 
 struct WinUnit {
   int b, h, hk;
+  int dh;         // query tile t is of head h + t * dh
   int q_start, q_end, k_start, k_end;
   int q_row0;
   int off;        // position of query i is i + off
@@ -72,7 +76,7 @@ struct WinUnit {
   int nsteps;
   int j0, j1;     // the steps of this item: all, or (KPAD) a range of them
   int place;      // -1: o and lse are written; else the item's place for partial results
-  int lse_base;
+  int lse_base, lse_next;  // of query tile t: lse_base + t * lse_next
   bool run, nokeys;
   bool rows[kQT];    // tile t has rows
   bool active[kQT];  // tile t has rows and sees keys of these steps
@@ -90,8 +94,11 @@ struct WinParams {
   int full;                    // 1: no causal border
   int by_block;                // 1: units numbered query block by query block
   int whole;                   // KPAD: units are not cut (see WinItem)
-  int num_mblocks;             // ceil(Nq / (kBR * kQT))
-  int num_units;               // B * H * num_mblocks
+  int pair;                    // 1: the query tiles of a unit are the same rows of two heads
+  int unit_rows;               // query rows of a unit in its sequence: kBR * kQT, or kBR (pair)
+  int unit_heads;              // units across the heads: H, or H / 2 (pair)
+  int num_mblocks;             // ceil(Nq / unit_rows)
+  int num_units;               // B * unit_heads * num_mblocks
   int total_q, total_k;        // variable-length form: packed rows (sequences past them are rejected)
   const int* cu_q;             // variable-length form: int32 [B + 1]
   const int* cu_k;             // KPAD: key lengths, int32 [B]
@@ -108,6 +115,11 @@ struct WinParams {
   unsigned long long timeout_ns;
   int* status;
 };
+
+// Row of the unit (0 .. 255) that holds packed row `row` of query tile t.
+__device__ __forceinline__ int win_unit_row(const WinUnit& w, int t, int row) {
+  return row - w.q_row0 + (w.dh ? t * kBR : 0);
+}
 
 // Restricts a unit to the steps [j0, j1).
 __device__ __forceinline__ void win_restrict(WinUnit& w, int j0, int j1, int place) {
@@ -132,12 +144,13 @@ __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
   // over units of falling work even.
   int mb = u % p.num_mblocks, r = u / p.num_mblocks;
   if (p.by_block) {
-    mb = u / (p.B * p.H);
-    r = u % (p.B * p.H);
+    mb = u / (p.B * p.unit_heads);
+    r = u % (p.B * p.unit_heads);
   }
   if (VARLEN || p.by_block) mb = p.num_mblocks - 1 - mb;
-  w.h = r % p.H;
-  w.b = r / p.H;
+  w.dh = p.pair;
+  w.h = (r % p.unit_heads) << p.pair;
+  w.b = r / p.unit_heads;
   w.hk = w.h / p.group;
   w.q_start = 0;
   w.q_end = p.Nq;
@@ -160,15 +173,16 @@ __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
           (VARLEN && w.q_start > p.total_q - len_q) || (VARLEN && !KPAD && w.k_start > p.total_k - len_k);
   }
   const int len_k = bad ? 0 : w.k_end - w.k_start;
-  w.q_row0 = w.q_start + mb * (kBR * kQT);
+  w.q_row0 = w.q_start + mb * p.unit_rows;
   w.off = (w.k_end - w.k_start) - (w.q_end - w.q_start);
   w.lse_base = (w.b * p.H + w.h) * p.Nq;
+  w.lse_next = p.pair ? p.Nq : 0;
   const bool has_rows = !bad && w.q_row0 < w.q_end;
   const int nsk = (min(p.sinks, len_k) + BC - 1) / BC;  // key tiles that hold sinks
   int first = 0x7fffffff, end = -1, lo[kQT], hi[kQT];
 #pragma unroll
   for (int t = 0; t < kQT; ++t) {
-    const int r0 = w.q_row0 + t * kBR;
+    const int r0 = w.q_row0 + (p.pair ? 0 : t * kBR);
     w.qwin[t] = make_window<VARLEN>(w.q_start, w.q_end, r0, kBR);
     w.rows[t] = has_rows && r0 < w.q_end;
     // Positions of the tile's first and last row of its own.
@@ -228,7 +242,7 @@ struct WinSmem {
 constexpr int kUnitCost = 2;
 template <bool VARLEN>
 __device__ __forceinline__ int win_flat(const WinParams& p, int b, int mb) {
-  const WinUnit w = win_decode<128, VARLEN, true>(p, b * p.H * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - mb : mb));
+  const WinUnit w = win_decode<128, VARLEN, true>(p, b * p.unit_heads * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - mb : mb));
   return w.rows[0] ? kUnitCost + max(w.nsteps, 1) : 0;
 }
 
@@ -332,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto flat = [&](int b) -> long long {
       long long sum = 0;
       for (int mb = 0; mb < p.num_mblocks; ++mb) sum += win_flat<VARLEN>(p, b, mb);
-      return sum * p.H;
+      return sum * p.unit_heads;
     };
     long long mine = 0;
     for (int b = b0; b < b1; ++b) mine += flat(b);
@@ -411,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       auto range_item = [&]() -> WinItem {
         while (pos < end) {
-          while (pos >= kat + static_cast<long long>(kw) * p.H) {
-            kat += static_cast<long long>(kw) * p.H;
+          while (pos >= kat + static_cast<long long>(kw) * p.unit_heads) {
+            kat += static_cast<long long>(kw) * p.unit_heads;
             if (++kmb == p.num_mblocks) {
               kmb = 0;
               ++kb;
@@ -425,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pos += to - at;
           const int j0 = max(at - kUnitCost, 0), j1 = to - kUnitCost;
           if (j1 <= j0) continue;  // the range ends ahead of the unit's first step
-          const int u = (kb * p.H + h) * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - kmb : kmb);
+          const int u = (kb * p.unit_heads + h) * p.num_mblocks + (VARLEN ? p.num_mblocks - 1 - kmb : kmb);
           const int c = static_cast<int>(blockIdx.x);
           if (j0 > 0 && to == kw) p.cut[c] = make_int2(u, static_cast<int>(step0 / span));
           return WinItem{u, j0, j1, j0 > 0 ? 2 * c : to < kw ? 2 * c + 1 : -1};
@@ -456,9 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int pnl = 0; pnl < kDPanels; ++pnl) {
               const uint32_t dst = base + L::kOffQ + t * L::kQTileBytes + pnl * L::kQPanelBytes;
               if constexpr (VARLEN)
-                ptx::tma_load_3d(dst, &tm_q, bar(L::kBarQFull), pnl * kPanel, w.h, w.qwin[t].load_row);
+                ptx::tma_load_3d(dst, &tm_q, bar(L::kBarQFull), pnl * kPanel, w.h + t * w.dh, w.qwin[t].load_row);
               else
-                ptx::tma_load_4d(dst, &tm_q, bar(L::kBarQFull), pnl * kPanel, w.h, w.qwin[t].load_row, w.b);
+                ptx::tma_load_4d(dst, &tm_q, bar(L::kBarQFull), pnl * kPanel, w.h + t * w.dh, w.qwin[t].load_row, w.b);
             }
           }
           auto load_tile = [&](uint32_t dst0, const CUtensorMap* tm, uint32_t full, int kt) {
@@ -612,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowWindow qw = t == 0 ? w.qwin[0] : w.qwin[1];
       // Place of this row's partial results (row of the unit).
       const size_t part = KPAD && w.place >= 0
-                              ? static_cast<size_t>(w.place) * (kBR * kQT) + (qw.load_row + row - w.q_row0)
+                              ? static_cast<size_t>(w.place) * (kBR * kQT) + win_unit_row(w, t, qw.load_row + row)
                               : 0;
       if (!(t == 0 ? w.active[0] : w.active[1])) {
         // No key of these steps in sight: a part of weight zero.
@@ -771,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool has = l > 0.f;
       s_invl[t * kBR + row] = has ? 1.f / l : 0.f;
       if (row >= qw.lo && row < qw.hi) {
-        float* const dst = KPAD && w.place >= 0 ? p.part_lse + part : p.lse + w.lse_base + (qw.load_row - w.q_start + row);
+        float* const dst = KPAD && w.place >= 0 ? p.part_lse + part : p.lse + w.lse_base + t * w.lse_next + (qw.load_row - w.q_start + row);
         *dst = has ? m_ref * p.scale + log2f(l) * 0.69314718055994530942f : -INFINITY;
       }
       ptx::mbar_arrive(bar(L::kBarLReady + t));
@@ -788,24 +802,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool pending = false;  // a TMA store from the staging area may still be reading it
     bool ok = true;
     // Rows without a visible key: o = 0, LSE = -inf.
-    auto zero_rows = [&](const WinUnit& w, int row0, int rows) {
+    auto zero_rows = [&](const WinUnit& w, int t, int row0, int rows) {
       const size_t rs = static_cast<size_t>(p.H) * D;
       const size_t first = VARLEN ? static_cast<size_t>(row0) : static_cast<size_t>(w.b) * p.Nq + row0;
       for (int e = threadIdx.x - 256; e < rows * (D / 8); e += 128)
-        ptx::st_global_v4(p.o + (first + e / (D / 8)) * rs + static_cast<size_t>(w.h) * D + (e % (D / 8)) * 8, 0u, 0u, 0u, 0u);
-      for (int r = threadIdx.x - 256; r < rows; r += 128) p.lse[w.lse_base + (row0 - w.q_start) + r] = -INFINITY;
+        ptx::st_global_v4(p.o + (first + e / (D / 8)) * rs + static_cast<size_t>(w.h + t * w.dh) * D + (e % (D / 8)) * 8, 0u, 0u, 0u, 0u);
+      for (int r = threadIdx.x - 256; r < rows; r += 128) p.lse[w.lse_base + t * w.lse_next + (row0 - w.q_start) + r] = -INFINITY;
     };
 #pragma unroll 1
     FA_WIN_FOR_EACH_ITEM(it) {
       FA_WIN_UNIT(it)
       if (w.nokeys) {
-        zero_rows(w, w.q_row0, min(kBR * kQT, w.q_end - w.q_row0));
+        for (int t = 0; t <= w.dh; ++t) zero_rows(w, t, w.q_row0, min(p.unit_rows, w.q_end - w.q_row0));
         continue;
       }
 #pragma unroll
       for (int t = 0; t < kQT; ++t) {
         const RowWindow qw = w.qwin[t];
-        if (w.rows[t] && !w.active[t] && !(KPAD && w.place >= 0)) zero_rows(w, qw.load_row + qw.lo, qw.hi - qw.lo);
+        if (w.rows[t] && !w.active[t] && !(KPAD && w.place >= 0)) zero_rows(w, t, qw.load_row + qw.lo, qw.hi - qw.lo);
         if (!w.active[t]) continue;
         if (!ptx::mbar_wait_warp(bar(L::kBarLReady + t), uc[t] & 1u, s_abort, tmo) ||
             !ptx::mbar_wait_warp(bar(L::kBarOFinal + t), uc[t] & 1u, s_abort, tmo)) {
@@ -822,10 +836,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool use_tma = !parted && (!VARLEN || warp_full);  // dense: rows past Nq are clipped by the map
         const bool row_ok = row >= qw.lo && row < qw.hi;
         __nv_bfloat16* const grow =
-            row_ok ? p.o + (static_cast<size_t>(qw.load_row + row) * p.H + w.h) * D : p.o;
+            row_ok ? p.o + (static_cast<size_t>(qw.load_row + row) * p.H + w.h + t * w.dh) * D : p.o;
         float* const prow =
             parted && row_ok
-                ? p.part_o + (static_cast<size_t>(w.place) * (kBR * kQT) + (qw.load_row + row - w.q_row0)) * D
+                ? p.part_o + (static_cast<size_t>(w.place) * (kBR * kQT) + win_unit_row(w, t, qw.load_row + row)) * D
                 : nullptr;
         if (use_tma && pending) {
           if (lane == 0) ptx::bulk_wait_group_read_0();
@@ -875,9 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int pnl = 0; pnl < kDPanels; ++pnl) {
               if constexpr (VARLEN)
-                ptx::tma_store_3d(&tm_o, stage + pnl * 4096, pnl * kPanel, w.h, qw.load_row + (wq << 5));
+                ptx::tma_store_3d(&tm_o, stage + pnl * 4096, pnl * kPanel, w.h + t * w.dh, qw.load_row + (wq << 5));
               else
-                ptx::tma_store_4d(&tm_o, stage + pnl * 4096, pnl * kPanel, w.h, qw.load_row + (wq << 5), w.b);
+                ptx::tma_store_4d(&tm_o, stage + pnl * 4096, pnl * kPanel, w.h + t * w.dh, qw.load_row + (wq << 5), w.b);
             }
             ptx::bulk_commit_group();
           }
@@ -909,7 +923,8 @@ __global__ void __launch_bounds__(256) fa_win_join_kernel(const WinParams p) {
   if (cut.x < 0) return;
   const WinUnit w = win_decode<128, VARLEN, true>(p, cut.x);
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (w.q_row0 + r >= w.q_end) return;
+  const int t = w.dh ? r / kBR : 0, i = w.q_row0 + (w.dh ? r % kBR : r);  // head of the unit, query row
+  if (i >= w.q_end) return;
   const int parts = static_cast<int>(blockIdx.x) - cut.y + 1;
   constexpr int kPer = D / 32;
   auto at = [&](int s) -> size_t { return (2 * static_cast<size_t>(cut.y + s) + (s == 0 ? 1 : 0)) * (kBR * kQT) + r; };
@@ -934,12 +949,12 @@ __global__ void __launch_bounds__(256) fa_win_join_kernel(const WinParams p) {
     }
   }
   const float il = l > 0.f ? 1.f / l : l;
-  const size_t row = VARLEN ? static_cast<size_t>(w.q_row0 + r) : static_cast<size_t>(w.b) * p.Nq + w.q_row0 + r;
-  __nv_bfloat16* const dst = p.o + (row * p.H + w.h) * D + lane * kPer;
+  const size_t row = VARLEN ? static_cast<size_t>(i) : static_cast<size_t>(w.b) * p.Nq + i;
+  __nv_bfloat16* const dst = p.o + (row * p.H + w.h + t) * D + lane * kPer;
 #pragma unroll
   for (int e = 0; e < kPer; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack_bf16x2(acc[e] * il, acc[e + 1] * il);
-  if (lane == 0) p.lse[w.lse_base + (w.q_row0 - w.q_start) + r] = l > 0.f ? M + logf(l) : l == 0.f ? -INFINITY : l;
+  if (lane == 0) p.lse[w.lse_base + t * w.lse_next + (i - w.q_start)] = l > 0.f ? M + logf(l) : l == 0.f ? -INFINITY : l;
 }
 
 }  // namespace fa

@@ -31,7 +31,7 @@ cudaError_t launch_win(const WinLaunchArgs& a) {
   if constexpr (KPAD) {
     const cudaError_t le = launch_dependent(kern, dim3(grid), kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
     if (le != cudaSuccess || a.p.whole) return le;
-    const dim3 rows(grid, (std::min(a.p.Nq, kBR * kQT) + 7) / 8);
+    const dim3 rows(grid, a.p.pair ? kBR * kQT / 8 : (std::min(a.p.Nq, kBR * kQT) + 7) / 8);
     return launch_dependent(&fa_win_join_kernel<D, VARLEN>, rows, 256, 0, a.stream, a.p);
   }
   kern<<<grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
@@ -140,8 +140,11 @@ int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v,
   if ((e = encode_rows(&a.tm_k, k, kpacked, p.B, nk, Hk, d, 128)) != FA_OK) return e;
   if ((e = encode_rows(&a.tm_v, v, kpacked, p.B, nk, Hk, d, 128)) != FA_OK) return e;
   p.group = p.H / Hk;
-  p.num_mblocks = (p.Nq + kBR * kQT - 1) / (kBR * kQT);
-  const long long units = static_cast<long long>(p.B) * p.H * p.num_mblocks;
+  p.pair = p.group % 2 == 0;
+  p.unit_rows = p.pair ? kBR : kBR * kQT;
+  p.unit_heads = p.pair ? p.H / 2 : p.H;
+  p.num_mblocks = (p.Nq + p.unit_rows - 1) / p.unit_rows;
+  const long long units = static_cast<long long>(p.B) * p.unit_heads * p.num_mblocks;
   if (units > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   p.num_units = static_cast<int>(units);
   // A window longer than the keys changes nothing and is cut to them, so that
