@@ -153,7 +153,7 @@ int check_sizes(int B, int total_q, int max_q, int max_k, int H, int Hk, int d, 
   if (H > 65535 || B > 65535) return FA_ERR_INVALID_ARG;
   const long long lim = 0x7fffffffLL;
   if (static_cast<long long>(B) * H * max_q > lim || static_cast<long long>(num_pages) * Hk * page > lim ||
-      static_cast<long long>(B) * (max_k + 127LL) > lim || max_k > lim - kKvTile)
+      static_cast<long long>(B) * (max_k + 127LL) > lim || max_k > lim - kKvTile || max_q > lim - 2 * 128)
     return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
@@ -266,8 +266,8 @@ int fa_fwd_kvcache(const void* q, const void* k8, const void* v8, const float* k
   dq.window = win;
   dq.sinks = snk;
   dq.status = dev.status;
-  if (z.k_pad > 0) {
-    const dim3 grid(z.k_pad / 64, B, 2);
+  {
+    const dim3 grid(std::max(z.k_pad / 64, 1), B, 2);  // without keys it still checks the lengths
     if (d == 128)
       fa::fa_kv_dequant_kernel<128><<<grid, 256, 0, st>>>(dq);
     else

@@ -385,6 +385,9 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
         if (id >= 0) {
           ks = p.k_scale[ph];
           vs = p.v_scale[ph];
+          // A page that was never written has scale 0: its codes are weighed with the
+          // smallest scale there is, so that its keys still count in the normaliser.
+          if (vs == 0.f) vs = __uint_as_float(static_cast<uint32_t>(kKvMinExp + 127) << 23);
         }
         if (!ptx::mbar_wait_warp(empty(st), ((done / L::kStages) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
           if (lane == 0) record_error(p.status, kErrTimeout, kKvSiteLoad);

@@ -90,6 +90,7 @@ int check_sizes(int B, int Nq, int Nk, int H, int Hk, int d, float scale, int wi
   if (misaligned(cu_q, 4) || misaligned(cu_k, 4)) return FA_ERR_ALIGN;
   if (H > 65535 || B > 65535) return FA_ERR_INVALID_ARG;
   const long long lim = 0x7fffffffLL;
+  if (Nq > lim - 2 * kBR || Nk > lim - 2 * kBR) return FA_ERR_INVALID_ARG;  // rounding up to tiles stays in 32 bits
   if (static_cast<long long>(B) * Nq > lim || static_cast<long long>(B) * Nk > lim ||
       static_cast<long long>(B) * H * Nq > lim)
     return FA_ERR_INVALID_ARG;

@@ -360,7 +360,9 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
  *   k8, v8           : uint8 [num_pages, Hk, page, d] e4m3 codes; page 16, 32, 64 or 128.
  *   k_scale, v_scale : fp32 [num_pages, Hk]; a code c of the page stands for
  *                      c * scale.  The append writes powers of two from 2^-64 to
- *                      2^120.
+ *                      2^120.  Scales are finite and not negative; 0 (a page never
+ *                      written) stands for values of 0.  V's scales of the pages that
+ *                      one query sees lie within 2^96 of one another.
  *   block_table      : int32 [B, table_width]; token t of sequence b lies in page
  *                      block_table[b][t / page], slot t % page.  Only entries up to
  *                      a sequence's last token are read.
@@ -401,7 +403,10 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
  *   o, lse  : as fa_fwd_ex (lse fp32 [B, H, max_seqlen_q], entries past a
  *             sequence's queries not written); rows without keys get 0 and -inf.
  *   q is used in full bf16 precision; weights are rounded to f16 (short queries)
- *   or bf16.  Slots behind the last token may hold anything.
+ *   or bf16.  Scales that are no powers of two are used as they are by short
+ *   queries, and round the values to bf16 in long chunks.  Slots behind the last
+ *   token may hold anything; tokens that some query of the sequence sees hold no
+ *   NaN (a weight of zero times NaN would reach the queries that do not see it).
  *   workspace : fa_kvcache_workspace_bytes(...) bytes of device memory, 16-byte
  *             aligned, rewritten by every call (NULL when 0); calls that share one
  *             must not overlap on the GPU.  Its size depends on the current device.

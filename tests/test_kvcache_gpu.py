@@ -359,6 +359,40 @@ def test_many_splits_and_loose_bound():
     _attend_and_check([90, 9000], 1, 4, 1, 64, 128, max_k=40_000)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 150])
+def test_pages_that_were_never_written(n, d):
+    """Scale 0: keys and values of 0.  Every key of such pages has score 0 and counts."""
+    Hk, H, page, m = 2, 4, 32, 300
+    c, table = _full_cache([m], Hk, page, d, 5)
+    empty = table[0, [1, 2, 7]].long()
+    for t in (c.k8, c.v8, c.k_scale, c.v_scale):
+        t[empty] = 0
+    q = _rand((1, n, H, d), 6)
+    o, lse = fa.forward_kvcache(q, c, table, _ints([m]), m)
+    _status()
+    k, v = _values(c, table, 0, m)
+    vs = c.v_scale[table[0].long()].max().item()
+    ref, lref, bound = _reference(q[0], k, v, vs, 1 / math.sqrt(d), R.visible(n, m, 0, 0, device="cuda"), n * H // Hk <= 128)
+    R.check(o[0], ref, bound, "o")
+    R.check_lse(lse[0], lref, "lse")
+    o, lse = fa.forward_kvcache(q, fa.KvCache.empty(c.num_pages, page, Hk, d), table, _ints([m]), m)
+    _status()
+    assert (o == 0).all()
+    R.check_lse(lse[0], torch.log(torch.arange(m - n + 1, m + 1, device="cuda").double()).expand(H, n), "lse of an empty cache")
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_lengths_against_no_keys_at_all(n):
+    c, table = _full_cache([64, 64, 64], 2, 16, 64, 1)
+    q = _rand((3, n, 4, 64), 2)
+    o, lse = fa.forward_kvcache(q, c, table, _ints([0, 0, 0]), 0)
+    _status()
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    fa.forward_kvcache(q, c, table, _ints([0, 0, 3]), 0)
+    _status(fa.FA_ERR_BAD_SEQLENS)
+
+
 def test_rows_behind_the_last_sequence_are_left():
     c, table = _full_cache([40, 300], 2, 16, 64, 5)
     for new in ([3, 2], [150, 200]):

@@ -55,6 +55,7 @@ def test_empty_append(L, kw):
     (dict(k8=0), BAD), (dict(vs=0), BAD), (dict(table=0), BAD), (dict(lens=0), BAD), (dict(q=MIS), ALI),
     (dict(v8=MIS), ALI), (dict(ws=MIS), ALI), (dict(lse=A + 2), ALI), (dict(table=A + 2), ALI),
     (dict(num_pages=1 << 28), BAD), (dict(max_k=0x7fffffff, B=1, total_q=3), BAD),
+    (dict(max_q=0x7fffffff, B=1, total_q=0x7fffffff, H=1, Hk=1), BAD),
 ])
 def test_attention_refusals(L, kw, code):
     assert fa.fa_fwd_kvcache(*dict(ATTEND, **kw).values()) == code

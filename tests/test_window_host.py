@@ -35,6 +35,7 @@ REFUSED = [
     (dict(cu_q=A + 2, cu_k=A, total_q=9, total_k=9), fa.FA_ERR_ALIGN), (dict(q=0), fa.FA_ERR_INVALID_ARG),
     (dict(v=MIS), fa.FA_ERR_ALIGN), (dict(lse=A + 2), fa.FA_ERR_ALIGN), (dict(Nk=0), fa.FA_ERR_INVALID_ARG),
     (dict(H=70000, Hk=70000), fa.FA_ERR_INVALID_ARG), (dict(B=40000, Nq=65536), fa.FA_ERR_INVALID_ARG),
+    (dict(H=1, Hk=1, Nq=0x7fffffff), fa.FA_ERR_INVALID_ARG), (dict(Nk=0x7fffffff), fa.FA_ERR_INVALID_ARG),
 ]
 
 
