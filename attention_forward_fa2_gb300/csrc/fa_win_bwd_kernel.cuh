@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ============================================================ TMA loads
       uint32_t g = 0, uc = 0;
       bool ok = true;
+      grid_dependency_wait();  // what the prep kernel writes is read, and added to, behind the first copy
 #pragma unroll 1
       FA_WIN_BWD_FOR_EACH_UNIT(u) {
         const WinBwdUnit w = win_bwd_decode<VARLEN>(p, u);
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::bulk_load(sld + kBwdBQ * 4, p.delta + ro, kBwdBQ * 4, fb);
         }
       }
+      grid_dependents_launch();  // the kernels behind this one may be set up; they wait for its end
       // Drain: every issued copy must land before the CTA exits.
       if (uc > 0) ptx::mbar_wait_drain(bar(L::kBarKVFull), (uc - 1) & 1u, tmo);
       for (uint32_t s = 0; s < STAGES; ++s) {
@@ -634,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows without keys, carry -inf, so that their P and dS are 0.
 template <int D, bool VARLEN>
 __global__ void __launch_bounds__(256) fa_win_prep_kernel(const WinBwdParams p) {
+  grid_dependents_launch();
   constexpr int kLanes = D / 8;
   const long long row = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
@@ -679,6 +682,7 @@ __global__ void __launch_bounds__(256) fa_win_prep_kernel(const WinBwdParams p) 
 // dq = bf16(scale * accumulator).
 template <int D, bool VARLEN>
 __global__ void __launch_bounds__(256) fa_win_dq_kernel(const WinBwdParams p) {
+  grid_dependency_wait();
   constexpr int kLanes = D / 8;
   const long long row = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
@@ -707,6 +711,8 @@ __global__ void __launch_bounds__(256) fa_win_dq_kernel(const WinBwdParams p) {
 // bound by reading the parts once (a few MB).
 template <int D, bool VARLEN>
 __global__ void __launch_bounds__(256) fa_win_sink_kernel(const WinBwdParams p) {
+  grid_dependents_launch();
+  grid_dependency_wait();
   const int keys = p.num_skb * kBwdBK;
   const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;

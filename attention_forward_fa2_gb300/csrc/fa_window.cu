@@ -70,10 +70,25 @@ cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
   static std::atomic<unsigned long long> done{0};
   e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
-  if (a.grid.x > 0) kern<<<a.grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_do, p);
+  // Each kernel is set up while the one before it ends, and waits for its end before it
+  // reads what that one wrote.  The key-block kernel clears dK and dV rows that nothing
+  // sees without that wait, so without a prep kernel before it it starts in order.
+  if (a.grid.x > 0) {
+    if (prep > 0)
+      e = launch_dependent(kern, a.grid, kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_do, p);
+    else
+      kern<<<a.grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_do, p);
+    if (e != cudaSuccess) return e;
+  }
   const long long sink_rows = static_cast<long long>(p.B) * p.Hk * p.num_skb * kBwdBK;
-  if (sink_rows > 0) fa_win_sink_kernel<D, VARLEN><<<static_cast<unsigned>((sink_rows + 7) / 8), 256, 0, a.stream>>>(p);
-  if (dq > 0) fa_win_dq_kernel<D, VARLEN><<<static_cast<unsigned>((dq + kRows - 1) / kRows), 256, 0, a.stream>>>(p);
+  if (sink_rows > 0) {
+    e = launch_dependent(&fa_win_sink_kernel<D, VARLEN>, dim3(static_cast<unsigned>((sink_rows + 7) / 8)), 256, 0, a.stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  if (dq > 0) {
+    e = launch_dependent(&fa_win_dq_kernel<D, VARLEN>, dim3(static_cast<unsigned>((dq + kRows - 1) / kRows)), 256, 0, a.stream, p);
+    if (e != cudaSuccess) return e;
+  }
   return cudaGetLastError();
 }
 
