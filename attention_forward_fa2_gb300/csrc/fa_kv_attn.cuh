@@ -14,6 +14,11 @@
 // the lengths, computes the units that lie in it whole, and leaves the ones cut
 // by its borders in fp32 in the workspace (at most two); a second kernel joins
 // them ("GPU 内核与 FlashAttention" §11.2).
+// Cluster form (ONE), for few units of few steps, where latency is all: a unit is a
+// cluster of up to 8 CTAs, each takes a share of its steps and leaves its part in its
+// own shared memory; the cluster's warps join them row by row through distributed
+// shared memory.  One launch, no workspace, no scan (one token, 16 heads on 4 of
+// d 128: 1000 keys 9.8 -> 8.4 us, batch 8 on 32/8 heads and 2000 keys 15.9 -> 11.7).
 //
 // A CTA: warp 4 walks the range ahead of the others, fills a ring of key tiles by
 // TMA, a page at a time (each lane looks up and loads one page of the tile), and
@@ -62,6 +67,7 @@ struct KvAttnParams {
   int B, max_q, max_k, total_q, H, Hk, G;
   int width, page, num_pages;
   int causal, window, sinks;
+  int cluster, row_groups;  // cluster form: CTAs and row groups (see there)
   float scale_log2;
   // Workspace: a unit cut by the borders of CTA c's range is at place 2c (begun by
   // an earlier CTA) or 2c + 1 (begun by c, ended later); cut[c] names the unit
@@ -106,7 +112,8 @@ struct KvSmem {
   static constexpr int kOffBar = kOffUnit + 2 * kUnitBytes;
   static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int kOffScan = kOffBar + kNumBars * 8;          // 6 long long, 2 long long, abort
-  static constexpr int kBytes = kOffScan + 80;
+  static constexpr int kOffLse = kOffScan + 80;                    // cluster form: of this CTA's part
+  static constexpr int kBytes = kOffLse + kRows * 4;
   static constexpr int kAlloc = kBytes + 1024;
   // At the end of a unit its last stage takes two warps' rows: d floats, m and l.
   static constexpr int kRowStride = D + 16;                        // floats; rows of a quarter-warp in different banks
@@ -195,7 +202,27 @@ __device__ __forceinline__ int kv_perm(int n) {
   return D == 128 ? (n >> 1) + ((n & 1) << 2) : n;
 }
 
-template <int D, int NT>
+// Where a unit of the cluster form stands, for the rows' end.
+struct KvPlace {
+  int b, hk, r0, rows, row0;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Address of this CTA's shared `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+template <int D, int NT, bool ONE>
 __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
     fa_kv_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const KvAttnParams p) {
@@ -216,6 +243,7 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
   const uint32_t meet_bar = base + L::kOffBar + 8u * (2 * L::kStages + 4);
   long long* const s_scan = reinterpret_cast<long long*>(gbase + L::kOffScan);  // warp sums, then (sequence, its first step)
   volatile int* const s_abort = reinterpret_cast<volatile int*>(gbase + L::kOffScan + 64);
+  float* const s_lse = reinterpret_cast<float*>(gbase + L::kOffLse);
   if (threadIdx.x == 0) {
     *s_abort = 0;
     for (int s = 0; s < L::kStages; ++s) {
@@ -229,6 +257,10 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
     ptx::mbar_init(meet_bar, 4);
     ptx::fence_mbar_init();
   }
+  long long begin = 0, end = 1, span = 1;
+  if constexpr (ONE) {
+    __syncthreads();
+  } else {
   // ------------------------------------------ this CTA's range of the steps of all units
   const int per = (p.B + kKvThreads - 1) / kKvThreads;  // sequences of a thread
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
@@ -253,8 +285,9 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
     total += s_scan[w];
   }
   pre -= mine;  // steps before this thread's sequences
-  const long long span = (total + gridDim.x - 1) / gridDim.x;
-  const long long begin = blockIdx.x * span, end = min(total, begin + span);
+  span = (total + gridDim.x - 1) / gridDim.x;
+  begin = blockIdx.x * span;
+  end = min(total, begin + span);
   if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (begin >= end) return;  // the whole CTA
   if (begin >= pre && begin < pre + mine) {
@@ -269,26 +302,45 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
     s_scan[7] = at;
   }
   __syncthreads();
+  }
 
-  if (warp == 4) {
+  auto load = [&]() {
     // ================================================================ loads
-    int b = static_cast<int>(s_scan[6]);
-    long long at = s_scan[7];  // first step of sequence b
+    int b = ONE ? 0 : static_cast<int>(s_scan[6]);
+    long long at = ONE ? 0 : s_scan[7];  // first step of sequence b
     long long pos = begin;
     const int ppt = kKvTile / p.page;  // pages per tile: one per lane
     int done = 0, units = 0;
     bool ok = true;
     while (ok && pos < end) {
-      KvSeq s = kv_seq<kRows>(p, b);
-      while (pos >= at + kv_flat(p, s)) {
-        at += kv_flat(p, s);
-        s = kv_seq<kRows>(p, ++b);
+      KvSeq s;
+      int steps, t0, t1, hk, r0;
+      if constexpr (ONE) {
+        const int u = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+        r0 = u % p.row_groups * kRows;
+        hk = u / p.row_groups % p.Hk;
+        b = u / p.row_groups / p.Hk;
+        s = kv_seq<kRows>(p, b);
+        if (s.bad && lane == 0 && hk == 0 && r0 == 0 && rank == 0) record_error(p.status, kErrBadSeqlens, 0);
+        if (lane == 0) *reinterpret_cast<KvPlace*>(s_scan) = KvPlace{b, hk, r0, s.rows, s.row0};
+        steps = s.steps();
+        t0 = steps * rank / p.cluster;
+        t1 = steps * (rank + 1) / p.cluster;
+        if (r0 >= s.rows || t0 == t1) break;
+      } else {
+        s = kv_seq<kRows>(p, b);
+        while (pos >= at + kv_flat(p, s)) {
+          at += kv_flat(p, s);
+          s = kv_seq<kRows>(p, ++b);
+        }
+        steps = s.steps();
+        const long long local = pos - at;
+        const int unit = static_cast<int>(local / steps);
+        t0 = static_cast<int>(local - static_cast<long long>(unit) * steps);
+        t1 = static_cast<int>(min(static_cast<long long>(steps), t0 + (end - pos)));
+        hk = unit / s.units_per_head;
+        r0 = (unit % s.units_per_head) * kRows;
       }
-      const int steps = s.steps();
-      const long long local = pos - at;
-      const int unit = static_cast<int>(local / steps), t0 = static_cast<int>(local - static_cast<long long>(unit) * steps);
-      const int t1 = static_cast<int>(min(static_cast<long long>(steps), t0 + (end - pos)));
-      const int hk = unit / s.units_per_head, r0 = (unit % s.units_per_head) * kRows;
       // ---- the unit and its queries, as B fragments: k-step kk = 4 h + wd takes
       // d = 16 (c + 4 h) + 4 wd + {0, 1 | 2, 3} of row 8 nt + g.
       uint4 raw[NT][D / 64][2];  // read ahead of the first tile's copies, laid out behind them
@@ -323,8 +375,8 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
           u->ns = s.range.ns;
           u->gap = s.range.gap;
           u->t0 = t0;
-          u->place = t0 > 0 ? 2 * blockIdx.x : t1 < steps ? 2 * blockIdx.x + 1 : -1;
-          if (t0 > 0 && t1 == steps)
+          u->place = ONE ? 0 : t0 > 0 ? 2 * blockIdx.x : t1 < steps ? 2 * blockIdx.x + 1 : -1;
+          if (!ONE && t0 > 0 && t1 == steps)
             p.cut[blockIdx.x] = make_int4(b, hk, r0, static_cast<int>((pos - t0) / span));
         }
         {
@@ -415,20 +467,20 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
           break;
         }
       }
-      pos += t1 - t0;
+      pos += ONE ? 1 : t1 - t0;
     }
     // The end of the units.
     if (ok && ptx::mbar_wait_warp(q_empty(units & 1), ((units >> 1) & 1u) ^ 1u, s_abort, p.timeout_ns)) {
       if (lane == 0) reinterpret_cast<KvUnit*>(gbase + L::kOffUnit + (units & 1) * L::kUnitBytes)->b = -1;
       ptx::mbar_arrive(q_full(units & 1));
     }
-    grid_dependents_launch();  // the join's blocks may be set up; they wait for this grid's end
+    if constexpr (!ONE) grid_dependents_launch();  // the join's blocks may be set up; they wait for this grid's end
     // Nothing may land in shared memory after the CTA is gone.
     for (int s = 0; s < L::kStages; ++s)
       if (done > s) ptx::mbar_wait_drain(full(s), ((done - 1 - s) / L::kStages) & 1u, p.timeout_ns);
-    return;
-  }
+  };
 
+  auto compute = [&]() {
   // ================================================================ compute
   const int page_shift = 31 - __clz(p.page);
   int done = 0;
@@ -700,7 +752,13 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
           const float lt = l[nt][e];
           const float il = lt > 0.f ? 1.f / lt : lt;  // NaN stays
           const float lse2 = lt > 0.f ? m[nt][e] + log2f(lt) : lt == 0.f ? -INFINITY : lt;
-          if (w.place >= 0) {
+          if constexpr (ONE) {
+            float* const part = reinterpret_cast<float*>(gbase) + (8 * nt + 2 * c + e) * D + 2 * g;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+              *reinterpret_cast<float2*>(part + 16 * k) = make_float2(acc[nt][k][e] * il, acc[nt][k][2 + e] * il);
+            if (g == 0) s_lse[8 * nt + 2 * c + e] = lse2;
+          } else if (w.place >= 0) {
             const size_t row = static_cast<size_t>(w.place) * kRows + 8 * nt + 2 * c + e;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
@@ -721,6 +779,53 @@ __global__ void __launch_bounds__(kKvThreads, (kKvCtas<D, NT>))
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(empty(last));
+  }
+  };
+
+  if (ONE && warp == 0 && lane < kRows) s_lse[lane] = -INFINITY;  // stays where the CTA has no steps
+  if (warp == 4)
+    load();
+  else
+    compute();
+  if constexpr (ONE) {
+    // ------------------------------------- the cluster's parts, row by row
+    __syncwarp();
+    cluster_sync();  // every thread of the cluster comes here: each wait above ends
+    const KvPlace u = *reinterpret_cast<const KvPlace*>(s_scan);
+    const int rank = blockIdx.x % p.cluster;
+    for (int r = rank + p.cluster * warp; r < kRows && u.r0 + r < u.rows; r += p.cluster * (kKvThreads / 32)) {
+      const float mine = lane < p.cluster ? ld_cluster(cluster_addr(ptx::smem_u32(s_lse + r), lane)) : -INFINITY;
+      float M = mine;
+#pragma unroll
+      for (int k = 4; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+      M = __shfl_sync(0xffffffffu, M, 0);
+      const float f = mine == -INFINITY ? 0.f : ptx::ex2(mine - M);
+      constexpr int kPer = D / 32;
+      float acc[kPer], l = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+      for (int s = 0; s < p.cluster; ++s) {
+        const float fs = __shfl_sync(0xffffffffu, f, s);
+        const bool none = __shfl_sync(0xffffffffu, mine, s) == -INFINITY;  // no values in that part
+        const uint32_t src = cluster_addr(base + (r * D + lane * kPer) * 4, s);
+        l += fs;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const float x = ld_cluster(src + 4 * e);
+          acc[e] = none ? acc[e] : fmaf(fs, x, acc[e]);
+        }
+      }
+      const float il = l > 0.f ? 1.f / l : l;  // NaN stays
+      const int i = (u.r0 + r) / p.G, h = u.hk * p.G + (u.r0 + r) % p.G;
+      __nv_bfloat16* const dst = p.o + (static_cast<size_t>(u.row0 + i) * p.H + h) * D + lane * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack_bf16x2(acc[e] * il, acc[e + 1] * il);
+      if (lane == 0)
+        p.lse[(static_cast<size_t>(u.b) * p.H + h) * p.max_q + i] =
+            l > 0.f ? (M + log2f(l)) * 0.69314718055994530942f : l == 0.f ? -INFINITY : l;
+    }
+    cluster_sync();  // no CTA leaves while another reads its parts
   }
 }
 
