@@ -115,7 +115,8 @@ cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const KvAtt
 // bf16 copy [B, k_pad, Hk, d] of the key tiles that some query sees, zeros behind
 // the sequence's end up to the tile's: with power-of-two scales the copy is exact,
 // so the products that follow see the values the codes stand for.  One block per
-// (64 tokens, sequence, K or V); bound by its bytes (1 read, 2 written a value).
+// (64 tokens, sequence, K or V); bound by its bytes (1 read, 2 written a value: 75 MB for
+// three sequences of 8192 keys, 4 heads of d 128, 13 us).
 struct DequantParams {
   const uint8_t *k8, *v8;
   const float *k_scale, *v_scale;
@@ -148,33 +149,54 @@ __global__ void __launch_bounds__(256) fa_kv_dequant_kernel(const DequantParams 
   const uint8_t* const codes = is_k ? p.k8 : p.v8;
   const float* const scales = is_k ? p.k_scale : p.v_scale;
   __nv_bfloat16* const out = is_k ? p.k : p.v;
-  for (int e = threadIdx.x; e < 64 * p.Hk * kLanes; e += 256) {
-    const int ch = e % kLanes;
-    const int t = t0 + (e / kLanes) % 64, hk = e / kLanes / 64;
-    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (t < len) {
-      const int id = p.table[static_cast<size_t>(b) * p.width + t / p.page];
-      if (kv_page_ok(id, p.num_pages)) {
-        const size_t ph = static_cast<size_t>(id) * p.Hk + hk;
-        const float s = scales[ph];
-        const uint4 raw = *reinterpret_cast<const uint4*>(codes + (ph * p.page + t % p.page) * D + 16 * ch);
-        const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+  // A thread's tokens and, four heads at a time, its loads are in flight together.
+  constexpr int kTok = 256 / kLanes, kPass = 64 / kTok;
+  const int ch = threadIdx.x % kLanes;
+  int id[kPass];
+#pragma unroll
+  for (int n = 0; n < kPass; ++n) {
+    const int t = t0 + n * kTok + threadIdx.x / kLanes;
+    id[n] = t < len ? p.table[static_cast<size_t>(b) * p.width + t / p.page] : -1;
+    if (t < len && !kv_page_ok(id[n], p.num_pages)) {
+      if (ch == 0) record_error(p.status, kErrBadPage, 0);
+      id[n] = -1;
+    }
+  }
+  for (int hk0 = 0; hk0 < p.Hk; hk0 += 4) {
+    uint4 raw[kPass][4];
+    float s[kPass][4];
+#pragma unroll
+    for (int n = 0; n < kPass; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const bool in = id[n] >= 0 && hk0 + g < p.Hk;
+        const int t = t0 + n * kTok + threadIdx.x / kLanes;
+        const size_t ph = in ? static_cast<size_t>(id[n]) * p.Hk + hk0 + g : 0;
+        s[n][g] = in ? scales[ph] : 0.f;
+        raw[n][g] = in ? *reinterpret_cast<const uint4*>(codes + (ph * p.page + t % p.page) * D + 16 * ch)
+                       : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int n = 0; n < kPass; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (hk0 + g >= p.Hk) continue;
+        const uint32_t v[4] = {raw[n][g].x, raw[n][g].y, raw[n][g].z, raw[n][g].w};
+        uint32_t w[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t lo, hi;
           e4m3x4_to_f16(v[k], lo, hi);
           const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
           const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          w[2 * k] = ptx::pack_bf16x2(a.x * s, a.y * s);
-          w[2 * k + 1] = ptx::pack_bf16x2(c.x * s, c.y * s);
+          w[2 * k] = ptx::pack_bf16x2(a.x * s[n][g], a.y * s[n][g]);
+          w[2 * k + 1] = ptx::pack_bf16x2(c.x * s[n][g], c.y * s[n][g]);
         }
-      } else if (ch == 0) {
-        record_error(p.status, kErrBadPage, 0);
+        const int t = t0 + n * kTok + threadIdx.x / kLanes;
+        __nv_bfloat16* const dst = out + ((static_cast<size_t>(b) * p.k_pad + t) * p.Hk + hk0 + g) * D + 16 * ch;
+        ptx::st_global_v4(dst, w[0], w[1], w[2], w[3]);
+        ptx::st_global_v4(dst + 8, w[4], w[5], w[6], w[7]);
       }
-    }
-    __nv_bfloat16* const dst = out + ((static_cast<size_t>(b) * p.k_pad + t) * p.Hk + hk) * D + 16 * ch;
-    ptx::st_global_v4(dst, w[0], w[1], w[2], w[3]);
-    ptx::st_global_v4(dst + 8, w[4], w[5], w[6], w[7]);
   }
 }
 
