@@ -95,7 +95,8 @@ struct WinParams {
   int by_block;                // 1: units numbered query block by query block
   int whole;                   // KPAD: units are not cut (see WinItem)
   int pair;                    // 1: the query tiles of a unit are the same rows of two heads
-  int unit_rows;               // query rows of a unit in its sequence: kBR * kQT, or kBR (pair)
+  int tiles;                   // query tiles of a unit: 2, or 1 (few units)
+  int unit_rows;               // query rows of a unit in its sequence: kBR * kQT, or kBR (pair, one tile)
   int unit_heads;              // units across the heads: H, or H / 2 (pair)
   int num_mblocks;             // ceil(Nq / unit_rows)
   int num_units;               // B * unit_heads * num_mblocks
@@ -184,7 +185,7 @@ __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
   for (int t = 0; t < kQT; ++t) {
     const int r0 = w.q_row0 + (p.pair ? 0 : t * kBR);
     w.qwin[t] = make_window<VARLEN>(w.q_start, w.q_end, r0, kBR);
-    w.rows[t] = has_rows && r0 < w.q_end;
+    w.rows[t] = has_rows && r0 < w.q_end && t < p.tiles;
     // Positions of the tile's first and last row of its own.
     const int p0 = p.full ? len_k - 1 : w.qwin[t].load_row - w.q_start + w.qwin[t].lo + w.off;
     const int p1 = p.full ? len_k - 1 : w.qwin[t].load_row - w.q_start + w.qwin[t].hi - 1 + w.off;

@@ -58,14 +58,14 @@ int encode_rows(CUtensorMap* m, const void* ptr, bool packed, int B, int n, int 
   return host_encode(m, ptr, packed ? 3 : 4, dims, strides, box);
 }
 
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, bool SPLIT>
 cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
   cudaError_t e = cudaSuccess;
   constexpr int kRows = 256 / (D / 8);
   const long long prep = static_cast<long long>(p.B) * p.H * p.nq_pad;
   const long long dq = static_cast<long long>(p.B) * p.H * p.Nq;
   if (prep > 0) fa_win_prep_kernel<D, VARLEN><<<static_cast<unsigned>((prep + kRows - 1) / kRows), 256, 0, a.stream>>>(p);
-  auto* kern = &fa_win_bwd_kernel<D, kWinBwdStages<D>, VARLEN>;
+  auto* kern = &fa_win_bwd_kernel<D, kWinBwdStages<D>, VARLEN, SPLIT>;
   constexpr int smem = BwdSmem<D, kWinBwdStages<D>>::kAlloc;
   static std::atomic<unsigned long long> done{0};
   e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
@@ -80,9 +80,9 @@ cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
       kern<<<a.grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_do, p);
     if (e != cudaSuccess) return e;
   }
-  const long long sink_rows = static_cast<long long>(p.B) * p.Hk * p.num_skb * kBwdBK;
-  if (sink_rows > 0) {
-    e = launch_dependent(&fa_win_sink_kernel<D, VARLEN>, dim3(static_cast<unsigned>((sink_rows + 7) / 8)), 256, 0, a.stream, p);
+  const long long sum_rows = static_cast<long long>(p.B) * p.Hk * (p.split > 1 ? p.num_kb : p.num_skb) * kBwdBK;
+  if (sum_rows > 0) {
+    e = launch_dependent(&fa_win_sum_kernel<D, VARLEN, SPLIT>, dim3(static_cast<unsigned>((sum_rows + 7) / 8)), 256, 0, a.stream, p);
     if (e != cudaSuccess) return e;
   }
   if (dq > 0) {
@@ -90,6 +90,11 @@ cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
+}
+
+template <int D, bool VARLEN>
+cudaError_t dispatch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
+  return p.split > 1 ? launch_win_bwd<D, VARLEN, true>(a, p) : launch_win_bwd<D, VARLEN, false>(a, p);
 }
 
 // Checks shared by the forward and the backward entry.
@@ -113,9 +118,30 @@ int check_sizes(int B, int Nq, int Nk, int H, int Hk, int d, float scale, int wi
 }
 
 struct BwdSizes {
-  int nq_pad, num_kb, num_skb, chunk_qb, num_chunks;
-  size_t dq_bytes, part_bytes;
+  int nq_pad, num_kb, num_skb, chunk_qb, num_chunks, split;
+  long long sink_units, units;
+  size_t dq_bytes, part_floats, part2_floats;
+  size_t bytes() const { return dq_bytes + 4 * (part_floats + part2_floats); }
 };
+
+// Parts of a unit: the fewest steps on the busiest of 152 SMs (this part's number,
+// so that the workspace depends on the sizes alone), where a unit's beginning and end
+// cost about kUnitSteps, the kernel that sums the parts kSumSteps, and the bytes of
+// 64 parts one step (2.9 us; 128 KB written and read a part of d 128).
+// Two sequences of 1024, 8 heads on 2 of d 64, no window: 74.9 us whole, 34.5 in parts.
+constexpr int kPlanSms = 152, kMaxSplit = 8, kUnitSteps = 1, kSumSteps = 2, kStepParts = 64;
+int bwd_split(long long units, long long steps) {
+  int best = 1;
+  long long least = 0;
+  for (int n = 1; n <= kMaxSplit && n <= steps; ++n) {
+    const long long rounds = (units * n + kPlanSms - 1) / kPlanSms;
+    const long long cost = rounds * ((steps + n - 1) / n + kUnitSteps) + (n > 1 ? kSumSteps + units * n / kStepParts : 0);
+    if (n > 1 && cost >= least) continue;
+    best = n;
+    least = cost;
+  }
+  return best;
+}
 
 // A chunk of a sink block walks as many query blocks as the other units do
 // (floor((window + 126) / 128) + 1), at least 4 so that short windows do not pay
@@ -129,7 +155,12 @@ BwdSizes bwd_sizes(int B, int Nq, int Nk, int H, int Hk, int d, int window, int 
   z.chunk_qb = std::max(4, (std::min(window, std::max(Nk, 1)) + 126) / kBwdBQ + 1);
   z.num_chunks = (blocks + z.chunk_qb - 1) / z.chunk_qb;
   z.dq_bytes = static_cast<size_t>(B) * H * z.nq_pad * (static_cast<size_t>(d) + 2) * 4;
-  z.part_bytes = static_cast<size_t>(z.num_chunks) * B * Hk * z.num_skb * kBwdBK * 2 * d * 4;
+  z.sink_units = static_cast<long long>(B) * Hk * z.num_skb * z.num_chunks;
+  z.units = z.sink_units + static_cast<long long>(B) * Hk * (z.num_kb - z.num_skb);
+  z.split = bwd_split(z.units, static_cast<long long>(Hk > 0 ? H / Hk : 1) * std::min(blocks, z.chunk_qb));
+  const size_t rows = static_cast<size_t>(z.split) * B * Hk * kBwdBK * 2 * d;  // of a key block
+  z.part_floats = rows * z.num_chunks * z.num_skb;
+  z.part2_floats = z.split > 1 ? rows * (z.num_kb - z.num_skb) : 0;
   return z;
 }
 
@@ -156,8 +187,13 @@ int launch_window(WinLaunchArgs& a, const void* q, const void* k, const void* v,
   if ((e = encode_rows(&a.tm_k, k, kpacked, p.B, nk, Hk, d, 128)) != FA_OK) return e;
   if ((e = encode_rows(&a.tm_v, v, kpacked, p.B, nk, Hk, d, 128)) != FA_OK) return e;
   p.group = p.H / Hk;
-  p.pair = p.group % 2 == 0;
-  p.unit_rows = p.pair ? kBR : kBR * kQT;
+  // One query tile a unit where the SMs take all of them at once (1000 queries, 8 heads
+  // of d 64, window 128: 12.2 -> 9.3 us; with more tiles than SMs two a unit take half
+  // again as long as one).
+  const long long tiles = static_cast<long long>(p.B) * p.H * ((p.Nq + kBR - 1) / kBR);
+  p.tiles = !kpad && tiles <= a.num_sms ? 1 : kQT;
+  p.pair = p.tiles == kQT && p.group % 2 == 0;
+  p.unit_rows = p.pair ? kBR : kBR * p.tiles;
   p.unit_heads = p.pair ? p.H / 2 : p.H;
   p.num_mblocks = (p.Nq + p.unit_rows - 1) / p.unit_rows;
   const long long units = static_cast<long long>(p.B) * p.unit_heads * p.num_mblocks;
@@ -227,7 +263,7 @@ long long fa_bwd_window_workspace_bytes(int B, int Nq, int Nk, int H, int Hk, in
   const int rc = fa::check_sizes(B, Nq, Nk, H, Hk, d, 1.f, window, sinks, nullptr, nullptr, 0, 0);
   if (rc != FA_OK) return rc;
   const fa::BwdSizes z = fa::bwd_sizes(B, Nq, Nk, H, Hk, d, window, sinks);
-  return static_cast<long long>(z.dq_bytes + z.part_bytes);
+  return static_cast<long long>(z.bytes());
 }
 
 int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
@@ -244,8 +280,8 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   if (rows_q > 0 && (!q || !o || !dout || !lse || !dq)) return FA_ERR_INVALID_ARG;
   const fa::BwdSizes z = fa::bwd_sizes(B, Nq, Nk, H, Hk, d, window, sinks);
   if (static_cast<long long>(B) * H * z.nq_pad > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  if (z.dq_bytes + z.part_bytes > 0 &&
-      (!workspace || workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < z.dq_bytes + z.part_bytes))
+  if (z.bytes() > 0 &&
+      (!workspace || workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < z.bytes()))
     return FA_ERR_INVALID_ARG;
   for (const void* ptr : {q, k, v, o, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
                           static_cast<const void*>(dv), static_cast<const void*>(workspace)})
@@ -269,11 +305,10 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   p.num_skb = z.num_skb;
   p.chunk_qb = z.chunk_qb;
   p.num_chunks = z.num_chunks;
-  const long long sink_units = static_cast<long long>(B) * Hk * z.num_skb * z.num_chunks;
-  const long long units = sink_units + static_cast<long long>(B) * Hk * (z.num_kb - z.num_skb);
-  if (units > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  p.num_sink_units = static_cast<int>(sink_units);
-  p.num_units = static_cast<int>(units);
+  if (z.units * z.split > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  p.split = z.split;
+  p.num_sink_units = static_cast<int>(z.sink_units * z.split);
+  p.num_units = static_cast<int>(z.units * z.split);
   p.window = std::min(window, std::max(Nk, 1));
   p.sinks = std::min(sinks, Nk);
   p.total_q = total_q;
@@ -286,6 +321,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   p.lse2 = p.dq_acc + rows_pad * d;
   p.delta = p.lse2 + rows_pad;
   p.part = p.delta + rows_pad;
+  p.part2 = p.part + z.part_floats;
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
@@ -310,9 +346,9 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   a.stream = static_cast<cudaStream_t>(stream);
   cudaError_t ce;
   if (d == 128)
-    ce = varlen ? fa::launch_win_bwd<128, true>(a, p) : fa::launch_win_bwd<128, false>(a, p);
+    ce = varlen ? fa::dispatch_win_bwd<128, true>(a, p) : fa::dispatch_win_bwd<128, false>(a, p);
   else
-    ce = varlen ? fa::launch_win_bwd<64, true>(a, p) : fa::launch_win_bwd<64, false>(a, p);
+    ce = varlen ? fa::dispatch_win_bwd<64, true>(a, p) : fa::dispatch_win_bwd<64, false>(a, p);
   return ce == cudaSuccess ? FA_OK : fa::host_cuda_fail(ce);
 }
 

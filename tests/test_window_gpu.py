@@ -71,6 +71,14 @@ def test_lengths_and_heads(B, Nq, Nk, H, Hk, d, window, sinks):
     _dense(B, Nq, Nk, H, Hk, d, window, sinks)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hk", [(6, 16, 8), (6, 8, 8), (4, 18, 6)])
+@pytest.mark.parametrize("window,sinks", [(150, 0), (300, 130)])
+def test_more_units_than_sms(B, H, Hk, d, window, sinks):
+    """Enough tiles that units are pairs of them, and key blocks are not cut into parts."""
+    _dense(B, 700, 750, H, Hk, d, window, sinks)
+
+
 def test_long_sequence_many_chunks_of_the_sink_block():
     _dense(1, 6000, 6000, 2, 1, 128, 200, 4)
 
@@ -104,20 +112,18 @@ def _packed(lens, H, Hk, d, seed=0, tail=5):
     return out, cu_q, cu_k, max(a for a, _ in lens), max(b for _, b in lens)
 
 
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("window,sinks", [(50, 0), (150, 130), (1000, 2)])
-def test_packed_sequences(d, window, sinks):
-    (q, k, v, do), cu_q, cu_k, mq, mk = _packed(LENS, 4, 2, d)
-    B, mark = len(LENS), 7.0
+def _packed_sequences(lens, H, Hk, d, window, sinks):
+    (q, k, v, do), cu_q, cu_k, mq, mk = _packed(lens, H, Hk, d)
+    B, mark = len(lens), 7.0
     kw = dict(cu_seqlens_q=cu_q, cu_seqlens_k=cu_k, max_seqlen_q=mq, max_seqlen_k=mk)
-    out, lse = torch.full_like(q, mark), torch.full((B, 4, mq), mark, device="cuda")
+    out, lse = torch.full_like(q, mark), torch.full((B, H, mq), mark, device="cuda")
     fa.forward_window(q, k, v, window, sinks, out=out, lse=lse, **kw)
     grads = [torch.full_like(t, mark) for t in (q, k, v)]
     fa.backward_window(q, k, v, out, lse, do, window, sinks, dq=grads[0], dk=grads[1], dv=grads[2], **kw)
     _ok()
     for t in (out, *grads):
         assert (t[-5:] == mark).all(), "rows behind the last sequence were written"
-    for b, (n, m) in enumerate(LENS):
+    for b, (n, m) in enumerate(lens):
         rq, rk = slice(int(cu_q[b]), int(cu_q[b]) + n), slice(int(cu_k[b]), int(cu_k[b]) + m)
         mask = R.visible(n, m, window, sinks, device="cuda")
         o_ref, lse_ref, bound = R.forward(q[rq], k[rk], v[rk], 1 / math.sqrt(d), mask)
@@ -127,6 +133,18 @@ def test_packed_sequences(d, window, sinks):
         ref, bounds = R.backward(q[rq], k[rk], v[rk], do[rq], 1 / math.sqrt(d), mask)
         for name, g, r, t in zip(("dq", "dk", "dv"), (grads[0][rq], grads[1][rk], grads[2][rk]), ref, bounds):
             R.check(g, r, t, "%s[%d]" % (name, b))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(50, 0), (150, 130), (1000, 2)])
+def test_packed_sequences(d, window, sinks):
+    _packed_sequences(LENS, 4, 2, d, window, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk", [(4, 2), (3, 3)])
+def test_many_packed_sequences(d, H, Hk):
+    _packed_sequences(LENS * 5, H, Hk, d, 150, 130)
 
 
 def test_gradients_are_those_of_differences():

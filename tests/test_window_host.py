@@ -47,13 +47,17 @@ def test_refusals(L, kw, code):
 
 def test_backward_workspace(L):
     def need(B, Nq, Nk, H, Hk, d, window, sinks):
-        pad = -(-Nq // 128) * 128
+        blocks, kb, skb = -(-Nq // 128), -(-Nk // 128), -(-min(sinks, Nk) // 128)
         chunk = max(4, (min(window, max(Nk, 1)) + 126) // 128 + 1)
-        chunks, skb = -(-pad // 128 // chunk) if pad else 0, -(-min(sinks, Nk) // 128)
-        chunks = -(-(pad // 128) // chunk)
-        return B * H * pad * (d + 2) * 4 + chunks * B * Hk * skb * 128 * 2 * d * 4
+        chunks = -(-blocks // chunk)
+        units, steps = B * Hk * (skb * chunks + kb - skb), H // Hk * min(blocks, chunk)
+        # Parts of a unit: the fewest steps on the busiest of 152 SMs.
+        split = min([(-(-units * n // 152) * (-(-steps // n) + 1) + (n > 1) * (2 + units * n // 64), n)
+                     for n in range(1, min(8, steps) + 1)] or [(0, 1)])[1]
+        rows = chunks * skb + (kb - skb if split > 1 else 0)
+        return B * H * blocks * 128 * (d + 2) * 4 + split * B * Hk * rows * 128 * 2 * d * 4
     for case in ((2, 100, 300, 4, 2, 64, 50, 0), (1, 5000, 5000, 4, 1, 128, 256, 4), (1, 5000, 5000, 4, 1, 128, 256, 300),
-                 (3, 0, 40, 2, 2, 64, 9, 4), (1, 700, 700, 2, 2, 128, 10 ** 9, 10 ** 9)):
+                 (3, 0, 40, 2, 2, 64, 9, 4), (1, 700, 700, 2, 2, 128, 10 ** 9, 10 ** 9), (8, 2000, 2000, 8, 8, 64, 100, 1)):
         assert fa.bwd_window_workspace_bytes(*case) == need(*case), case
     n = need(1, 64, 64, 4, 2, 128, 16, 2)
     assert fa.fa_bwd_window(*dict(BWD, ws_bytes=n - 1).values()) == fa.FA_ERR_INVALID_ARG
