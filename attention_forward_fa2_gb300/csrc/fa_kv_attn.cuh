@@ -42,8 +42,10 @@
 //   ldmatrix.trans on byte pairs, one byte permute apart from the A fragment; P
 //   turns from S^T's layout to the B fragment by movmatrix.  perm() places the two
 //   rows that a quarter-warp reads in different banks.
-//   Occupancy: two or three CTAs an SM: a warp's step is one dependent chain of loads, products, shuffles
-//   and exponentials, and other warps have to cover it.
+//   Measured: 64 sequences of 8192 keys, 32 heads on 8 of d 128, one token each: 165 us,
+//   97 % of a copy's bandwidth; four tokens each (16 rows) 193 us, 83 %.
+//   Occupancy: two or three CTAs an SM: a warp's step is one dependent chain of loads,
+//   products, shuffles and exponentials, and other warps have to cover it.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

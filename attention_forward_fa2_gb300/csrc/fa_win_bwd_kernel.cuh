@@ -21,6 +21,9 @@
 //     atomics: dK and dV come out the same on every run).
 //   Few units for the SMs: the steps (heads of the group times query blocks) of every
 //     unit are cut into `split` parts, handled like the chunks.
+// Bound by the chain of a step (see the MMA thread): two sequences of 4096, 16 heads on
+// 4 of d 128, window 512, 4 sinks: 119 us, tensor pipe 47 % busy; 155 us with the
+// kernels before and behind it.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
