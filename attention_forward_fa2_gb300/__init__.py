@@ -742,16 +742,22 @@ def _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqle
     device = _cuda_device("q", q)
     ndim, bf16 = 3 if packed else 4, _torch.bfloat16
     ptrs = _dense("q", q, bf16, ndim, device), _dense("k", k, bf16, ndim, device), _dense("v", v, bf16, ndim, device)
-    qs, ks = q.shape, k.shape
-    H, d = qs[-2:]
-    Hk = ks[-2]
-    if ks[-1] != d or v.shape != ks or (not packed and ks[0] != qs[0]):
+    ks = k.shape
+    if packed:
+        total_q, H, d = q.shape
+        total_k, Hk, dk = ks
+        same = True
+    else:
+        B, Nq, H, d = q.shape
+        Bk, Nk, Hk, dk = ks
+        same = B == Bk
+    if dk != d or v.shape != ks or not same:
         raise ValueError("q/k/v shape mismatch")
     if (Hk == 0 and H > 0) or (Hk > 0 and H % Hk):
         raise ValueError("query heads (%d) must be a multiple of key/value heads (%d)" % (H, Hk))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if not packed:
-        return device, ptrs, (qs[0], qs[1], ks[1], H, Hk, d, scale), (None, None, 0, 0)
+        return device, ptrs, (B, Nq, Nk, H, Hk, d, scale), (None, None, 0, 0)
     if cu_seqlens_q is None or cu_seqlens_k is None or max_seqlen_q is None or max_seqlen_k is None:
         raise ValueError("packed sequences need cu_seqlens_q/k and max_seqlen_q/k")
     cu = (_dense("cu_seqlens_q", cu_seqlens_q, _torch.int32, 1, device),
@@ -759,7 +765,7 @@ def _window_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqle
     B = cu_seqlens_q.numel() - 1
     if B < 0 or cu_seqlens_k.numel() != B + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k need B + 1 entries each")
-    return device, ptrs, (B, int(max_seqlen_q), int(max_seqlen_k), H, Hk, d, scale), cu + (qs[0], ks[0])
+    return device, ptrs, (B, int(max_seqlen_q), int(max_seqlen_k), H, Hk, d, scale), cu + (total_q, total_k)
 
 
 def _int32(x):
@@ -855,9 +861,10 @@ class KvCache:
         self._scales = (_dense("k_scale", k_scale, _torch.float32, 2, device),
                         _dense("v_scale", v_scale, _torch.float32, 2, device))
         shape = k8.shape
-        if v8.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
-            raise ValueError("codes are [num_pages, Hk, page, d], scales [num_pages, Hk]")
         self.num_pages, self.Hk, self.page, self.d = shape
+        pages = (self.num_pages, self.Hk)
+        if v8.shape != shape or k_scale.shape != pages or v_scale.shape != pages:
+            raise ValueError("codes are [num_pages, Hk, page, d], scales [num_pages, Hk]")
         self.k8, self.v8, self.k_scale, self.v_scale = k8, v8, k_scale, v_scale
 
     @classmethod
@@ -870,8 +877,8 @@ class KvCache:
 
 
 def _token_rows(name, t, ndim, device):
-    """Address of t [B, n, heads, d] or [total, heads, d], and the distance in elements between its
-    token rows."""
+    """Address and shape of t [B, n, heads, d] or [total, heads, d], and the distance in elements
+    between its token rows."""
     try:
         fine = t.dtype is _torch.bfloat16 and t.device == device and t.dim() == ndim
     except AttributeError:
@@ -884,24 +891,24 @@ def _token_rows(name, t, ndim, device):
             raise ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     shape = t.shape
-    heads, d = shape[-2:]
+    heads, d = shape[ndim - 2], shape[ndim - 1]
     if t.is_contiguous():
-        return t.data_ptr(), heads * d
+        return t.data_ptr(), shape, heads * d
     s = t.stride()
     if (d > 1 and s[-1] != 1) or (heads > 1 and s[-2] != d):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     if ndim == 3:
-        return t.data_ptr(), s[0] if shape[0] > 1 else heads * d
+        return t.data_ptr(), shape, s[0] if shape[0] > 1 else heads * d
     B, n = shape[:2]
     if B > 1 and n > 1 and s[0] != n * s[1]:
         raise ValueError("%s: tokens must be evenly spaced" % name)
-    return t.data_ptr(), s[1] if n > 1 else s[0] if B > 1 else heads * d
+    return t.data_ptr(), shape, s[1] if n > 1 else s[0] if B > 1 else heads * d
 
 
 def _sequences(name, lens, block_table, B, device):
     """Addresses of the lengths and the table, and the table's width."""
     ptr, table = _dense(name, lens, _torch.int32, 1, device), _dense("block_table", block_table, _torch.int32, 2, device)
-    if lens.shape[0] != B:
+    if lens.numel() != B:
         raise ValueError("%s needs %d entries" % (name, B))
     rows, width = block_table.shape
     if rows != B:
@@ -927,20 +934,20 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
     packed = cu_seqlens is not None
     ndim = 3 if packed else 4
     device = cache.device
-    kp, k_stride = _token_rows("k", k, ndim, device)
-    vp, v_stride = _token_rows("v", v, ndim, device)
-    shape = k.shape
-    Hk, d = shape[-2:]
-    if v.shape != shape or Hk != cache.Hk or d != cache.d:
+    kp, shape, k_stride = _token_rows("k", k, ndim, device)
+    vp, v_shape, v_stride = _token_rows("v", v, ndim, device)
+    Hk, d = shape[ndim - 2], shape[ndim - 1]
+    if v_shape != shape or Hk != cache.Hk or d != cache.d:
         raise ValueError("k, v and the cache differ in shape")
     cu = None
     if packed:
         cu = _dense("cu_seqlens", cu_seqlens, _torch.int32, 1, device)
         if max_seqlen is None:
             raise ValueError("max_seqlen is required with cu_seqlens")
-        B, total, n = cu_seqlens.shape[0] - 1, shape[0], int(max_seqlen)
+        B, total, n = cu_seqlens.numel() - 1, shape[0], int(max_seqlen)
+        tokens = (total,)
     else:
-        B, n = shape[:2]
+        tokens = B, n = shape[0], shape[1]
         total = B * n
     lens, table, width = _sequences("cache_lens", cache_lens, block_table, B, device)
     if (cos is None) != (sin is None):
@@ -956,11 +963,10 @@ def append_kvcache(cache, k, v, block_table, cache_lens, q=None, cos=None, sin=N
     H = q_stride = 0
     qp = qop = None
     if q is not None:
-        qp, q_stride = _token_rows("q", q, ndim, device)
-        qs = q.shape
-        if qs[:-2] != shape[:-2] or qs[-1] != d:
+        qp, qs, q_stride = _token_rows("q", q, ndim, device)
+        H = qs[ndim - 2]
+        if qs != (*tokens, H, d):
             raise ValueError("q and k differ in their tokens")
-        H = qs[-2]
         if q_out is None:
             q_out = _torch.empty(qs, dtype=_torch.bfloat16, device=device)
             qop = q_out.data_ptr()
@@ -998,8 +1004,11 @@ def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, c
     packed = cu_seqlens_q is not None
     device = cache.device
     qp = _dense("q", q, _torch.bfloat16, 3 if packed else 4, device)
-    shape = q.shape
-    H, d = shape[-2:]
+    if packed:
+        total, H, d = q.shape
+    else:
+        B, n, H, d = q.shape
+        total = B * n
     Hk = cache.Hk
     if d != cache.d:
         raise ValueError("q and the cache differ in head dimension")
@@ -1010,10 +1019,7 @@ def forward_kvcache(q, cache, block_table, seq_lens, max_seqlen_k, scale=None, c
         cu = _dense("cu_seqlens_q", cu_seqlens_q, _torch.int32, 1, device)
         if max_seqlen_q is None:
             raise ValueError("max_seqlen_q is required with cu_seqlens_q")
-        B, n, total = cu_seqlens_q.shape[0] - 1, int(max_seqlen_q), shape[0]
-    else:
-        B, n = shape[:2]
-        total = B * n
+        B, n = cu_seqlens_q.numel() - 1, int(max_seqlen_q)
     lens, table, width = _sequences("seq_lens", seq_lens, block_table, B, device)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     causal, window, sinks, max_k = 1 if causal else 0, _int32(window), _int32(sinks), int(max_seqlen_k)

@@ -54,10 +54,9 @@ KvPlan kv_plan(int B, int max_q, int max_k, int H, int Hk, int d, int causal, in
   z.rows = rows <= 8 ? 8 : 16;
   const long long resident = (z.rows == 8 || d == 64 ? 3 : kKvCtas<128, 2>) * num_sms;
   const long long units = B * static_cast<long long>(Hk) * ((rows + z.rows - 1) / z.rows);
-  int c = 1;
-  while (c < 8 && c < steps && 2 * c * units <= resident) c *= 2;
-  if (c * units <= resident && steps <= static_cast<long long>(kClusterSteps) * c) {
-    z.cluster = c;
+  const long long c = std::max<long long>(1, std::min({8LL, steps, units > 0 ? resident / units : 1}));
+  if (c * units <= resident && steps <= kClusterSteps * c) {
+    z.cluster = static_cast<int>(c);
     z.ctas = static_cast<int>(c * units);
     return z;
   }
