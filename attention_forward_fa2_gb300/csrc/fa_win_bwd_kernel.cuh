@@ -45,6 +45,7 @@ struct WinBwdParams : BwdParams {
   int split;           // parts of a unit
   int num_sink_units;  // B * Hk * num_skb * num_chunks * split
   int total_q, total_k;  // variable-length form: packed rows (sequences past them are rejected)
+  int* order;          // packed: the units that have work, the longest first; their number behind place num_units
   float* part;         // [num_chunks * split, B, Hk, num_skb * 128, 2 (dV, dK), d] fp32
   float* part2;        // split > 1: [split, B, Hk, (num_kb - num_skb) * 128, 2, d], the other blocks
 };
@@ -150,7 +151,7 @@ __device__ __forceinline__ WinBwdUnit win_bwd_decode(const WinBwdParams& p, int 
   w.b = r / p.Hk;
   bool bad;
   win_bwd_seq<VARLEN>(p, w.b, w.q_start, w.len_q, w.k_start, w.len_k, bad);
-  if (bad && threadIdx.x == 0)
+  if (bad)
     record_error(p.status, kErrBadSeqlens, 0);
   w.off = w.len_k - w.len_q;
   w.kw = make_window<VARLEN>(w.k_start, w.k_start + w.len_k, w.k_start + w.kb * kBwdBK, kBwdBK);
@@ -174,7 +175,49 @@ __device__ __forceinline__ WinBwdUnit win_bwd_decode(const WinBwdParams& p, int 
   return w;
 }
 
-#define FA_WIN_BWD_FOR_EACH_UNIT(u) for (int u = blockIdx.x; u < p.num_units && ok; u += gridDim.x)
+// The units of a CTA: round by round, packed ones (where listed) in the order of the
+// list, every other round from its end, so that units of falling length even out.
+#define FA_WIN_BWD_FOR_EACH_UNIT(u)                                                                              \
+  for (int round = 0, u = unit_at(0); round * static_cast<int>(gridDim.x) < num_units && ok; u = unit_at(++round)) \
+    if (u >= 0)
+
+// Lists the units that have work (one block; behind the list their number): a counting
+// sort by steps into 64 bins, the longest first.  Without it, ragged sequences leave
+// the static rounds uneven: nine of 386 to 2048 tokens, 2 key/value heads, window 300:
+// 43 steps on the busiest SM where 34 are possible.
+constexpr int kOrderMax = 16384;  // units up to which they are listed
+template <bool SPLIT>
+__device__ __forceinline__ void win_bwd_list(const WinBwdParams& p) {
+  constexpr int kBins = 64;
+  __shared__ int bins[kBins];
+  const int most = p.group * (p.nq_pad / kBwdBQ);
+  auto bin = [&](int u) -> int {  // -1: no work
+    const WinBwdUnit w = win_bwd_decode<true, SPLIT>(p, u);
+    if (w.kb * kBwdBK >= w.len_k || (w.nsteps == 0 && w.part >= 0)) return -1;
+    return kBins - 1 - static_cast<int>(static_cast<long long>(w.nsteps) * (kBins - 1) / max(most, 1));
+  };
+  if (threadIdx.x < kBins) bins[threadIdx.x] = 0;
+  __syncthreads();
+  for (int u = threadIdx.x; u < p.num_units; u += blockDim.x) {
+    const int b = bin(u);
+    if (b >= 0) atomicAdd(&bins[b], 1);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int sum = 0;
+    for (int b = 0; b < kBins; ++b) {
+      const int n = bins[b];
+      bins[b] = sum;
+      sum += n;
+    }
+    p.order[p.num_units] = sum;
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < p.num_units; u += blockDim.x) {
+    const int b = bin(u);
+    if (b >= 0) p.order[atomicAdd(&bins[b], 1)] = u;
+  }
+}
 
 template <int D, int STAGES, bool VARLEN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -247,6 +290,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
+  if constexpr (VARLEN) grid_dependency_wait();  // the prep kernel wrote the list
+  const bool listed = VARLEN && p.order != nullptr;
+  const int num_units = listed ? p.order[p.num_units] : p.num_units;
+  auto unit_at = [&](int round) -> int {
+    const int c = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x);
+    const int at = round * n + (listed && (round & 1) ? n - 1 - c : c);
+    return at >= num_units ? -1 : listed ? p.order[at] : at;
+  };
+
   // Handshake barriers are single: each one's next completion needs an action
   // of its own waiter first (S(g+1) is issued after P(g) is seen, dP(g+1)
   // after the drain has read dQ^T(g), which follows dS(g), and so on).
@@ -256,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ============================================================ TMA loads
       uint32_t g = 0, uc = 0;
       bool ok = true;
-      grid_dependency_wait();  // what the prep kernel writes is read, and added to, behind the first copy
+      if constexpr (!VARLEN) grid_dependency_wait();  // what it wrote is read, and added to, behind the first copy
 #pragma unroll 1
       FA_WIN_BWD_FOR_EACH_UNIT(u) {
         const WinBwdUnit w = win_bwd_decode<VARLEN, SPLIT>(p, u);
@@ -675,81 +727,100 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Before and after the key-block kernel.  Both give 16 (d = 128) or 8 (d = 64)
 // lanes to a row, 16 bytes of bf16 a lane, and are bound by their bytes (the
-// accumulator's 4 d, and 4 d of o and dout, a row).
+// accumulator's 4 d, and 4 d of o and dout, a row).  PASSES rows a group, 128 a block,
+// where most rows are those of no sequence (a long and many short packed ones).
 //
 // -D_i, the scaled log-sum-exp negated and a cleared accumulator row for every
 // entry of the tile order (see BwdParams): entries without a row of their own, and
 // rows without keys, carry -inf, so that their P and dS are 0.
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, bool SPLIT, int PASSES>
 __global__ void __launch_bounds__(256) fa_win_prep_kernel(const WinBwdParams p) {
   grid_dependents_launch();
   constexpr int kLanes = D / 8;
-  const long long row = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  uint32_t block = blockIdx.x;
+  if (VARLEN && p.order != nullptr && block-- == 0) {  // the first block lists the units
+    win_bwd_list<SPLIT>(p);
+    return;
+  }
   const int lane = threadIdx.x % kLanes;
-  const long long rows = static_cast<long long>(p.B) * p.H * p.nq_pad;
-  const bool in = row < rows;
-  const int t = in ? static_cast<int>(row % p.nq_pad) : 0;
-  const long long bh = in ? row / p.nq_pad : 0;
-  const int h = static_cast<int>(bh % p.H);
-  const int b = static_cast<int>(bh / p.H);
-  int q_start, len_q, k_start, len_k;
-  bool bad;
-  win_bwd_seq<VARLEN>(p, b, q_start, len_q, k_start, len_k, bad);
-  const int qb = t / kBwdBQ, c = t % kBwdBQ;
-  const RowWindow qw = make_window<VARLEN>(q_start, q_start + len_q, q_start + qb * kBwdBQ, kBwdBQ);
-  float acc = 0.f, l2 = INFINITY;
-  if (in && qb * kBwdBQ < len_q && c >= qw.lo && c < qw.hi) {
-    const int i = qw.load_row - q_start + c;
-    const size_t prow = VARLEN ? static_cast<size_t>(qw.load_row + c) : static_cast<size_t>(b) * p.Nq + i;
-    const size_t off = (prow * p.H + h) * D + lane * 8;
-    const uint4 a = *reinterpret_cast<const uint4*>(p.dout + off), o = *reinterpret_cast<const uint4*>(p.o + off);
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, ov[4] = {o.x, o.y, o.z, o.w};
+  const uint32_t rows = static_cast<uint32_t>(p.B) * p.H * p.nq_pad;  // less than 2^31
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc += __uint_as_float(av[e] << 16) * __uint_as_float(ov[e] << 16);
-      acc += __uint_as_float(av[e] & 0xffff0000u) * __uint_as_float(ov[e] & 0xffff0000u);
+  for (int pass = 0; pass < PASSES; ++pass) {
+    const uint32_t row = (block * PASSES + pass) * (256 / kLanes) + threadIdx.x / kLanes;
+    const bool in = row < rows;
+    const int t = in ? row % p.nq_pad : 0;
+    const uint32_t bh = in ? row / p.nq_pad : 0;
+    const int h = bh % p.H;
+    const int b = bh / p.H;
+    int q_start, len_q, k_start, len_k;
+    bool bad;
+    win_bwd_seq<VARLEN>(p, b, q_start, len_q, k_start, len_k, bad);
+    const int qb = t / kBwdBQ, c = t % kBwdBQ;
+    if (qb * kBwdBQ >= len_q) {  // a query block of no sequence: nobody reads it
+      if (PASSES > 1) return;    // the block's rows are those of one query block
+      continue;                  // and the warp's
     }
-    const float L = p.lse[static_cast<size_t>(bh) * p.Nq + i];
-    if (L > -INFINITY) l2 = L * 1.44269504088896340736f;
-    else acc = 0.f;
-  }
+    const RowWindow qw = make_window<VARLEN>(q_start, q_start + len_q, q_start + qb * kBwdBQ, kBwdBQ);
+    float acc = 0.f, l2 = INFINITY;
+    if (in && c >= qw.lo && c < qw.hi) {
+      const int i = qw.load_row - q_start + c;
+      const size_t prow = VARLEN ? static_cast<size_t>(qw.load_row + c) : static_cast<size_t>(b) * p.Nq + i;
+      const size_t off = (prow * p.H + h) * D + lane * 8;
+      const uint4 a = *reinterpret_cast<const uint4*>(p.dout + off), o = *reinterpret_cast<const uint4*>(p.o + off);
+      const uint32_t av[4] = {a.x, a.y, a.z, a.w}, ov[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-  for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-  if (!in) return;
-  if (lane == 0) {
-    p.delta[row] = -acc;
-    p.lse2[row] = -l2;
+      for (int e = 0; e < 4; ++e) {
+        acc += __uint_as_float(av[e] << 16) * __uint_as_float(ov[e] << 16);
+        acc += __uint_as_float(av[e] & 0xffff0000u) * __uint_as_float(ov[e] & 0xffff0000u);
+      }
+      const float L = p.lse[static_cast<size_t>(bh) * p.Nq + i];
+      if (L > -INFINITY) l2 = L * 1.44269504088896340736f;
+      else acc = 0.f;
+    }
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+    if (!in) continue;
+    if (lane == 0) {
+      p.delta[row] = -acc;
+      p.lse2[row] = -l2;
+    }
+    float* const dst = p.dq_acc + static_cast<size_t>(row) * D + lane * 4;
+    ptx::st_global_v4(dst, 0u, 0u, 0u, 0u);
+    ptx::st_global_v4(dst + D / 2, 0u, 0u, 0u, 0u);
   }
-  float* const dst = p.dq_acc + static_cast<size_t>(row) * D + lane * 4;
-  ptx::st_global_v4(dst, 0u, 0u, 0u, 0u);
-  ptx::st_global_v4(dst + D / 2, 0u, 0u, 0u, 0u);
 }
 
 // dq = bf16(scale * accumulator).
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, int PASSES>
 __global__ void __launch_bounds__(256) fa_win_dq_kernel(const WinBwdParams p) {
   grid_dependency_wait();
   constexpr int kLanes = D / 8;
-  const long long row = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
-  if (row >= static_cast<long long>(p.B) * p.H * p.Nq) return;
-  const int i = static_cast<int>(row % p.Nq);
-  const long long bh = row / p.Nq;
-  const int h = static_cast<int>(bh % p.H);
-  const int b = static_cast<int>(bh / p.H);
-  int q_start, len_q, k_start, len_k;
-  bool bad;
-  win_bwd_seq<VARLEN>(p, b, q_start, len_q, k_start, len_k, bad);
-  if (i >= len_q) return;
-  const int qb = i / kBwdBQ;
-  const RowWindow qw = make_window<VARLEN>(q_start, q_start + len_q, q_start + qb * kBwdBQ, kBwdBQ);
-  const int t = qb * kBwdBQ + (q_start + i - qw.load_row);
-  const size_t prow = VARLEN ? static_cast<size_t>(q_start + i) : static_cast<size_t>(b) * p.Nq + i;
-  const float4* src = reinterpret_cast<const float4*>(p.dq_acc + (static_cast<size_t>(bh) * p.nq_pad + t) * D + lane * 8);
-  const float4 x = src[0], y = src[1];
-  ptx::st_global_v4(p.dq + (prow * p.H + h) * D + lane * 8, ptx::pack_bf16x2(x.x * p.scale, x.y * p.scale),
-                    ptx::pack_bf16x2(x.z * p.scale, x.w * p.scale), ptx::pack_bf16x2(y.x * p.scale, y.y * p.scale),
-                    ptx::pack_bf16x2(y.z * p.scale, y.w * p.scale));
+#pragma unroll
+  for (int pass = 0; pass < PASSES; ++pass) {
+    const uint32_t row = (blockIdx.x * PASSES + pass) * (256 / kLanes) + threadIdx.x / kLanes;
+    if (row >= static_cast<uint32_t>(p.B) * p.H * p.nq_pad) return;
+    const int i = row % p.nq_pad;
+    const uint32_t bh = row / p.nq_pad;
+    const int h = bh % p.H;
+    const int b = bh / p.H;
+    int q_start, len_q, k_start, len_k;
+    bool bad;
+    win_bwd_seq<VARLEN>(p, b, q_start, len_q, k_start, len_k, bad);
+    if (i >= len_q) {
+      if (PASSES > 1 && i - i % kBwdBQ >= len_q) return;  // nor do the block's other rows
+      continue;
+    }
+    const int qb = i / kBwdBQ;
+    const RowWindow qw = make_window<VARLEN>(q_start, q_start + len_q, q_start + qb * kBwdBQ, kBwdBQ);
+    const int t = qb * kBwdBQ + (q_start + i - qw.load_row);
+    const size_t prow = VARLEN ? static_cast<size_t>(q_start + i) : static_cast<size_t>(b) * p.Nq + i;
+    const float4* src = reinterpret_cast<const float4*>(p.dq_acc + (static_cast<size_t>(bh) * p.nq_pad + t) * D + lane * 8);
+    const float4 x = src[0], y = src[1];
+    ptx::st_global_v4(p.dq + (prow * p.H + h) * D + lane * 8, ptx::pack_bf16x2(x.x * p.scale, x.y * p.scale),
+                      ptx::pack_bf16x2(x.z * p.scale, x.w * p.scale), ptx::pack_bf16x2(y.x * p.scale, y.y * p.scale),
+                      ptx::pack_bf16x2(y.z * p.scale, y.w * p.scale));
+  }
 }
 
 // dK and dV of the keys whose blocks are not one unit: the fp32 parts, added in

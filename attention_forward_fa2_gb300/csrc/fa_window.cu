@@ -58,13 +58,13 @@ int encode_rows(CUtensorMap* m, const void* ptr, bool packed, int B, int n, int 
   return host_encode(m, ptr, packed ? 3 : 4, dims, strides, box);
 }
 
-template <int D, bool VARLEN, bool SPLIT>
+template <int D, bool VARLEN, bool SPLIT, int PASSES>
 cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
   cudaError_t e = cudaSuccess;
-  constexpr int kRows = 256 / (D / 8);
+  constexpr int kRows = 256 / (D / 8) * PASSES;
   const long long prep = static_cast<long long>(p.B) * p.H * p.nq_pad;
-  const long long dq = static_cast<long long>(p.B) * p.H * p.Nq;
-  if (prep > 0) fa_win_prep_kernel<D, VARLEN><<<static_cast<unsigned>((prep + kRows - 1) / kRows), 256, 0, a.stream>>>(p);
+  const long long prep_blocks = (prep + kRows - 1) / kRows + (VARLEN && p.order ? 1 : 0);
+  if (prep_blocks > 0) fa_win_prep_kernel<D, VARLEN, SPLIT, PASSES><<<static_cast<unsigned>(prep_blocks), 256, 0, a.stream>>>(p);
   auto* kern = &fa_win_bwd_kernel<D, kWinBwdStages<D>, VARLEN, SPLIT>;
   constexpr int smem = BwdSmem<D, kWinBwdStages<D>>::kAlloc;
   static std::atomic<unsigned long long> done{0};
@@ -74,7 +74,7 @@ cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
   // reads what that one wrote.  The key-block kernel clears dK and dV rows that nothing
   // sees without that wait, so without a prep kernel before it it starts in order.
   if (a.grid.x > 0) {
-    if (prep > 0)
+    if (prep_blocks > 0)
       e = launch_dependent(kern, a.grid, kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_do, p);
     else
       kern<<<a.grid, kThreads, smem, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_do, p);
@@ -85,8 +85,8 @@ cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
     e = launch_dependent(&fa_win_sum_kernel<D, VARLEN, SPLIT>, dim3(static_cast<unsigned>((sum_rows + 7) / 8)), 256, 0, a.stream, p);
     if (e != cudaSuccess) return e;
   }
-  if (dq > 0) {
-    e = launch_dependent(&fa_win_dq_kernel<D, VARLEN>, dim3(static_cast<unsigned>((dq + kRows - 1) / kRows)), 256, 0, a.stream, p);
+  if (prep > 0) {
+    e = launch_dependent(&fa_win_dq_kernel<D, VARLEN, PASSES>, dim3(static_cast<unsigned>((prep + kRows - 1) / kRows)), 256, 0, a.stream, p);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
@@ -94,7 +94,12 @@ cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
 
 template <int D, bool VARLEN>
 cudaError_t dispatch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
-  return p.split > 1 ? launch_win_bwd<D, VARLEN, true>(a, p) : launch_win_bwd<D, VARLEN, false>(a, p);
+  // The rows of a packed batch are walked up to the longest length: blocks of more rows
+  // where three in four are of no sequence (4000 tokens and 40 x 100, 16 heads on 4 of
+  // d 128: 439 -> 169 us).
+  if (VARLEN && p.split == 1 && static_cast<long long>(p.B) * p.nq_pad > 4 * (p.total_q + 128LL * p.B))
+    return launch_win_bwd<D, VARLEN, false, VARLEN ? kBwdBQ / (256 / (D / 8)) : 1>(a, p);
+  return p.split > 1 ? launch_win_bwd<D, VARLEN, true, 1>(a, p) : launch_win_bwd<D, VARLEN, false, 1>(a, p);
 }
 
 // Checks shared by the forward and the backward entry.
@@ -121,7 +126,8 @@ struct BwdSizes {
   int nq_pad, num_kb, num_skb, chunk_qb, num_chunks, split;
   long long sink_units, units;
   size_t dq_bytes, part_floats, part2_floats;
-  size_t bytes() const { return dq_bytes + 4 * (part_floats + part2_floats); }
+  size_t order_bytes;  // of the list of units, behind all else
+  size_t bytes() const { return dq_bytes + 4 * (part_floats + part2_floats) + order_bytes; }
 };
 
 // Parts of a unit: the fewest steps on the busiest of 152 SMs (this part's number,
@@ -161,6 +167,7 @@ BwdSizes bwd_sizes(int B, int Nq, int Nk, int H, int Hk, int d, int window, int 
   const size_t rows = static_cast<size_t>(z.split) * B * Hk * kBwdBK * 2 * d;  // of a key block
   z.part_floats = rows * z.num_chunks * z.num_skb;
   z.part2_floats = z.split > 1 ? rows * (z.num_kb - z.num_skb) : 0;
+  z.order_bytes = z.units * z.split <= kOrderMax ? 4 * (static_cast<size_t>(z.units) * z.split + 1) : 0;
   return z;
 }
 
@@ -322,6 +329,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   p.delta = p.lse2 + rows_pad;
   p.part = p.delta + rows_pad;
   p.part2 = p.part + z.part_floats;
+  p.order = varlen && z.order_bytes > 0 ? reinterpret_cast<int*>(p.part2 + z.part2_floats) : nullptr;
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);

@@ -147,6 +147,12 @@ def test_many_packed_sequences(d, H, Hk):
     _packed_sequences(LENS * 5, H, Hk, d, 150, 130)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sinks", [0, 4])
+def test_one_long_and_many_short_sequences(d, sinks):
+    _packed_sequences([(9, 9), (0, 30)] * 10 + [(1800, 1900)] + [(130, 130), (1, 1)] * 12, 4, 2, d, 200, sinks)
+
+
 def test_gradients_are_those_of_differences():
     """Directional derivative of sum(o * dout) in 64 bits against the kernel's gradients."""
     d, n, window, sinks = 64, 200, 33, 3

@@ -55,7 +55,8 @@ def test_backward_workspace(L):
         split = min([(-(-units * n // 152) * (-(-steps // n) + 1) + (n > 1) * (2 + units * n // 64), n)
                      for n in range(1, min(8, steps) + 1)] or [(0, 1)])[1]
         rows = chunks * skb + (kb - skb if split > 1 else 0)
-        return B * H * blocks * 128 * (d + 2) * 4 + split * B * Hk * rows * 128 * 2 * d * 4
+        listed = 4 * (units * split + 1) if units * split <= 16384 else 0
+        return B * H * blocks * 128 * (d + 2) * 4 + split * B * Hk * rows * 128 * 2 * d * 4 + listed
     for case in ((2, 100, 300, 4, 2, 64, 50, 0), (1, 5000, 5000, 4, 1, 128, 256, 4), (1, 5000, 5000, 4, 1, 128, 256, 300),
                  (3, 0, 40, 2, 2, 64, 9, 4), (1, 700, 700, 2, 2, 128, 10 ** 9, 10 ** 9), (8, 2000, 2000, 8, 8, 64, 100, 1)):
         assert fa.bwd_window_workspace_bytes(*case) == need(*case), case
