@@ -349,6 +349,15 @@ def test_packed_queries(d, packed):
     _attend_and_check([5, 400, 77, 555], 0, 8, 2, d, 16, packed=packed)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,n,H,Hk,window,sinks", [(20, 1, 8, 4, 0, 0), (20, 3, 16, 4, 300, 4), (13, 2, 10, 5, 0, 0),
+                                                   (1, 1, 4, 1, 0, 0)])
+def test_few_units(B, n, H, Hk, d, window, sinks):
+    """Clusters of several sizes, some of whose members have no step of a short sequence."""
+    _attend_and_check([(997 * b + 700) % 1000 if b % 4 else 1000 for b in range(B)], n, H, Hk, d, 32, window=window,
+                      sinks=sinks, seed=11)
+
+
 def test_page_scales_that_differ_widely():
     for n in (1, 4):
         _attend_and_check([900, 200], n, 8, 2, 128, 16, spread=6.0)
