@@ -210,7 +210,7 @@ __device__ __forceinline__ WinUnit win_decode(const WinParams& p, int u) {
   for (int t = 0; t < kQT; ++t) w.st[t] = w.active[t] ? win_steps(lo[t], hi[t], nsk, w.ns, w.gap) : WinSteps{0, 0, 0};
   win_restrict(w, 0, w.nsteps, -1);
   if (bad && mb == 0 && w.h == 0) {
-    if ((threadIdx.x & 31) == 0 && threadIdx.x < 32) record_error(p.status, kErrBadSeqlens, 0);
+    if (threadIdx.x == 0 || threadIdx.x == 13 * 32) record_error(p.status, kErrBadSeqlens, 0);
   }
   return w;
 }
@@ -520,7 +520,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n_clc;
           clc_pending = false;
           cur.u = ptx::clc_cancelled_x(base + L::kOffClc);
-          if (!publish(cur)) break;
+          // Units without rows (packed batches are walked up to the longest length) go no
+          // further than here.
+          while (cur.u >= 0 && cur.u < p.num_units && !win_decode<BC, VARLEN, KPAD>(p, cur.u).rows[0]) {
+            request();
+            if (!ptx::mbar_wait(bar(L::kBarClc), n_clc & 1u, s_abort, tmo)) {
+              record_error(p.status, kErrTimeout, kSiteItem);
+              ok = false;
+              break;
+            }
+            ++n_clc;
+            clc_pending = false;
+            cur.u = ptx::clc_cancelled_x(base + L::kOffClc);
+          }
+          if (!ok || !publish(cur)) break;
           if (cur.u >= 0) request();
         } else {
           cur.u += gridDim.x;
