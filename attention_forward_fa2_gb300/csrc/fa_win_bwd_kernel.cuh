@@ -17,12 +17,12 @@
 //     kernel with one CTA per head running.  Its query blocks are cut into
 //     chunks of chunk_qb blocks (about a window's worth), one unit each; a
 //     chunk writes its dK and dV in fp32 to a place of its own in the
-//     workspace, and fa_win_sum_kernel adds the chunks in their order (no
+//     workspace, and the last kernel adds the chunks in their order (no
 //     atomics: dK and dV come out the same on every run).
 //   Few units for the SMs: the steps (heads of the group times query blocks) of every
 //     unit are cut into `split` parts, handled like the chunks.
 // Bound by the chain of a step (see the MMA thread): two sequences of 4096, 16 heads on
-// 4 of d 128, window 512, 4 sinks: 119 us, tensor pipe 47 % busy; 155 us with the
+// 4 of d 128, window 512, 4 sinks: 119 us, tensor pipe 47 % busy; 151 us with the
 // kernels before and behind it.
 #pragma once
 #include <cuda.h>
@@ -792,13 +792,12 @@ __global__ void __launch_bounds__(256) fa_win_prep_kernel(const WinBwdParams p) 
 
 // dq = bf16(scale * accumulator).
 template <int D, bool VARLEN, int PASSES>
-__global__ void __launch_bounds__(256) fa_win_dq_kernel(const WinBwdParams p) {
-  grid_dependency_wait();
+__device__ __forceinline__ void win_bwd_dq(const WinBwdParams& p, uint32_t block) {
   constexpr int kLanes = D / 8;
   const int lane = threadIdx.x % kLanes;
 #pragma unroll
   for (int pass = 0; pass < PASSES; ++pass) {
-    const uint32_t row = (blockIdx.x * PASSES + pass) * (256 / kLanes) + threadIdx.x / kLanes;
+    const uint32_t row = (block * PASSES + pass) * (256 / kLanes) + threadIdx.x / kLanes;
     if (row >= static_cast<uint32_t>(p.B) * p.H * p.nq_pad) return;
     const int i = row % p.nq_pad;
     const uint32_t bh = row / p.nq_pad;
@@ -827,11 +826,9 @@ __global__ void __launch_bounds__(256) fa_win_dq_kernel(const WinBwdParams p) {
 // their order, to bf16.  One warp per (sequence, key/value head, key);
 // bound by reading the parts once (a few MB).
 template <int D, bool VARLEN, bool SPLIT>
-__global__ void __launch_bounds__(256) fa_win_sum_kernel(const WinBwdParams p) {
-  grid_dependents_launch();
-  grid_dependency_wait();
+__device__ __forceinline__ void win_bwd_sum(const WinBwdParams& p, uint32_t block) {
   const int keys = (SPLIT ? p.num_kb : p.num_skb) * kBwdBK;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const long long row = static_cast<long long>(block) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= static_cast<long long>(p.B) * p.Hk * keys) return;
   const int key = static_cast<int>(row % keys);
@@ -874,6 +871,17 @@ __global__ void __launch_bounds__(256) fa_win_sum_kernel(const WinBwdParams p) {
   __nv_bfloat16* const dst = (lane < 16 ? p.dv : p.dk) + (prow * p.Hk + hk) * D + (lane & 15) * kPer;
 #pragma unroll
   for (int e = 0; e < kPer; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack_bf16x2(acc[e], acc[e + 1]);
+}
+
+// Behind the key-block kernel: the first sum_blocks blocks add parts, the others round
+// dQ; the sums' latency hides behind dQ's bytes.
+template <int D, bool VARLEN, bool SPLIT, int PASSES>
+__global__ void __launch_bounds__(256, 6) fa_win_finish_kernel(const WinBwdParams p, uint32_t sum_blocks) {
+  grid_dependency_wait();
+  if (blockIdx.x < sum_blocks)
+    win_bwd_sum<D, VARLEN, SPLIT>(p, blockIdx.x);
+  else
+    win_bwd_dq<D, VARLEN, PASSES>(p, blockIdx.x - sum_blocks);
 }
 
 }  // namespace fa

@@ -81,12 +81,11 @@ cudaError_t launch_win_bwd(const BwdLaunchArgs& a, const WinBwdParams& p) {
     if (e != cudaSuccess) return e;
   }
   const long long sum_rows = static_cast<long long>(p.B) * p.Hk * (p.split > 1 ? p.num_kb : p.num_skb) * kBwdBK;
-  if (sum_rows > 0) {
-    e = launch_dependent(&fa_win_sum_kernel<D, VARLEN, SPLIT>, dim3(static_cast<unsigned>((sum_rows + 7) / 8)), 256, 0, a.stream, p);
-    if (e != cudaSuccess) return e;
-  }
-  if (prep > 0) {
-    e = launch_dependent(&fa_win_dq_kernel<D, VARLEN, PASSES>, dim3(static_cast<unsigned>((prep + kRows - 1) / kRows)), 256, 0, a.stream, p);
+  const long long sum_blocks = (sum_rows + 7) / 8, blocks = sum_blocks + (prep + kRows - 1) / kRows;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (blocks > 0) {
+    e = launch_dependent(&fa_win_finish_kernel<D, VARLEN, SPLIT, PASSES>, dim3(static_cast<unsigned>(blocks)), 256, 0,
+                         a.stream, p, static_cast<uint32_t>(sum_blocks));
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
