@@ -31,6 +31,47 @@ struct KvPlan {
   size_t ws_bytes;
 };
 
+// The cluster form's launch.
+template <int D, int NT>
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute& a, int cluster, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(ctas);
+  c.blockDim = dim3(kKvThreads);
+  c.dynamicSmemBytes = KvSmem<D, NT>::kAlloc;
+  c.stream = stream;
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = cluster;
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  return c;
+}
+
+// Clusters of `c` CTAs that the device holds at once (fewer than its CTAs allow: a
+// cluster stays within one group of SMs; 64 clusters of 7 fit by number, but ran in
+// two rounds, 18.7 us where clusters of 4 took 10.0).  Asked once for each size.
+template <int D, int NT>
+int max_clusters(int c) {
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][c].load(std::memory_order_relaxed);
+  if (n == 0) {
+    auto* kern = &fa_kv_attn_kernel<D, NT, true>;
+    static std::atomic<unsigned long long> done{0};
+    if (set_smem_once(reinterpret_cast<const void*>(kern), KvSmem<D, NT>::kAlloc, done) != cudaSuccess) return 0;
+    cudaLaunchAttribute a;
+    const cudaLaunchConfig_t config = cluster_config<D, NT>(a, c, c, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &config) != cudaSuccess) {
+      cudaGetLastError();  // the equal ranges run instead
+      n = 0;
+    }
+    n = n > 0 ? n : -1;
+    known[dev][c].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // Steps of a CTA up to which the cluster form runs, where its units fit the SMs at once
 // (one token, 16 heads on 4 of d 128: 4000 keys, 4 steps, 11.1 us against 11.3 in equal
 // ranges; 8000 keys, 8 steps, 14.9 against 13.2).
@@ -54,8 +95,13 @@ KvPlan kv_plan(int B, int max_q, int max_k, int H, int Hk, int d, int causal, in
   z.rows = rows <= 8 ? 8 : 16;
   const long long resident = (z.rows == 8 || d == 64 ? 3 : kKvCtas<128, 2>) * num_sms;
   const long long units = B * static_cast<long long>(Hk) * ((rows + z.rows - 1) / z.rows);
-  const long long c = std::max<long long>(1, std::min({8LL, steps, units > 0 ? resident / units : 1}));
-  if (c * units <= resident && steps <= kClusterSteps * c) {
+  long long c = std::max<long long>(1, std::min({8LL, steps, units > 0 ? resident / units : 1}));
+  auto fits = [&](int n) -> bool {
+    return units <= (z.rows == 8 ? (d == 128 ? max_clusters<128, 1>(n) : max_clusters<64, 1>(n))
+                                 : (d == 128 ? max_clusters<128, 2>(n) : max_clusters<64, 2>(n)));
+  };
+  while (c >= 1 && steps <= kClusterSteps * c && !fits(static_cast<int>(c))) --c;
+  if (c >= 1 && steps <= kClusterSteps * c) {
     z.cluster = static_cast<int>(c);
     z.ctas = static_cast<int>(c * units);
     return z;
@@ -81,17 +127,8 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const KvAtt
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(ctas);
-  c.blockDim = dim3(kKvThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = stream;
   cudaLaunchAttribute a;
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim.x = p.cluster;
-  a.val.clusterDim.y = a.val.clusterDim.z = 1;
-  c.attrs = &a;
-  c.numAttrs = 1;
+  const cudaLaunchConfig_t c = cluster_config<D, NT>(a, p.cluster, ctas, stream);
   return cudaLaunchKernelEx(&c, kern, tk, tv, p);
 }
 
